@@ -15,7 +15,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcsa2.so")
 
 FULL, REINDEX, REINDEX_POOL, REUSE = 0, 1, 2, 3
-WS_INDEX, WS_ATTN, WS_GROUP, WS_STACK = 1, 2, 3, 4
+WS_INDEX, WS_ATTN, WS_GROUP, WS_STACK, WS_PAGED_ATTN, WS_BLOCK_TABLES = 1, 2, 3, 4, 5, 6
 GROUP_INPUTS_READY, GROUP_SERIAL = 1, 2
 FMT_BF16, FMT_FP8, FMT_MXFP4, FMT_NVFP4 = 0, 1, 2, 3
 ENTRY_BYTES = 288
@@ -75,6 +75,26 @@ class Io(ctypes.Structure):
     _fields_ = [("in_", ctypes.POINTER(Copy)), ("n_in", _c_i32), ("out", ctypes.POINTER(Copy)), ("n_out", _c_i32)]
 
 
+class BlockTableArgs(ctypes.Structure):
+    _fields_ = [("B", _c_i32), ("block_size", _c_i32), ("max_blocks", _c_i32), ("ld_table", _c_i64), ("len", _c_p),
+                ("n_new", _c_p), ("free_blocks", _c_p), ("n_free", _c_i32), ("free_pos", _c_p), ("block_table", _c_p),
+                ("len_out", _c_p), ("start", _c_p), ("slots", _c_p), ("max_new", _c_i64), ("info", _c_p)]
+
+
+class PagedRowsArgs(ctypes.Structure):
+    _fields_ = [("B", _c_i32), ("Q", _c_i32), ("K", _c_i32), ("block_size", _c_i32), ("max_blocks", _c_i32),
+                ("ld_table", _c_i64), ("n_blocks", _c_i64), ("positions", _c_p), ("n_vis", _c_p),
+                ("block_table", _c_p), ("rows", _c_p)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("B", _c_i32), ("Q", _c_i32), ("W", _c_i32), ("block_size", _c_i32), ("max_blocks", _c_i32),
+                ("ld_table", _c_i64), ("n_blocks", _c_i64), ("block_stride", _c_i64), ("q", _c_p), ("kv", _c_p),
+                ("kv_format", _c_i32), ("block_table", _c_p), ("n_vis", _c_p), ("swa", _c_p), ("swa_rows", _c_i32),
+                ("swa_step", _c_i32), ("swa_format", _c_i32), ("swa_scale", _c_p), ("scale", _c_f32), ("out", _c_p),
+                ("lse", _c_p)]
+
+
 _lib = None
 
 
@@ -98,6 +118,9 @@ def load(path=LIB_PATH):
     lib.csa2_stack_decode.argtypes = [ctypes.POINTER(StackArgs), _c_p, ctypes.c_size_t, _c_p]
     lib.csa2_group_decode_io.argtypes = [ctypes.POINTER(GroupArgs), ctypes.POINTER(Io), _c_p, ctypes.c_size_t, _c_p]
     lib.csa2_stack_decode_io.argtypes = [ctypes.POINTER(StackArgs), ctypes.POINTER(Io), _c_p, ctypes.c_size_t, _c_p]
+    lib.csa2_block_tables.argtypes = [ctypes.POINTER(BlockTableArgs), _c_p, ctypes.c_size_t, _c_p]
+    lib.csa2_paged_rows.argtypes = [ctypes.POINTER(PagedRowsArgs), _c_p]
+    lib.csa2_paged_attn.argtypes = [ctypes.POINTER(PagedAttnArgs), _c_p, ctypes.c_size_t, _c_p]
     lib.csa2_noalloc_scratch_bytes.argtypes = []
     lib.csa2_noalloc_scratch_bytes.restype = ctypes.c_size_t
     lib.csa2_workspace_size.argtypes = [_c_p, _c_i32]
@@ -117,6 +140,7 @@ def load(path=LIB_PATH):
                  "csa2_compress_rope_quantize_kv_fp4",
                  "csa2_index_score_topk", "csa2_index_score_topk_noalloc", "csa2_sparse_attn",
                  "csa2_group_decode", "csa2_stack_decode", "csa2_group_decode_io", "csa2_stack_decode_io",
+                 "csa2_block_tables", "csa2_paged_rows", "csa2_paged_attn",
                  "csa2_device_status", "csa2_trace_begin", "csa2_trace_stop",
                  "csa2_trace_end", "csa2_trace_get"):
         getattr(lib, name).restype = _c_i32
@@ -316,6 +340,133 @@ def csa2_group_decode_io(args, io, ws, stream=None):
 def csa2_stack_decode_io(args, io, ws, stream=None):
     _check(load().csa2_stack_decode_io(ctypes.byref(args), ctypes.byref(io), _ptr(ws),
                                        ws.numel() * ws.element_size(), _stream(stream)), "csa2_stack_decode_io")
+
+
+# ---------------------------------------------------------------------------
+# The paged cache
+# ---------------------------------------------------------------------------
+
+def _need(t, what, dtype, *shape):
+    """A dense tensor of this type and shape (None: any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _need_table(block_table, B):
+    """(max_blocks, ld_table) of an int32 [B, max_blocks] table whose rows may lie apart."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table: expected torch.int32 [{B}, max_blocks], got {block_table.dtype} "
+                         f"{list(block_table.shape)}")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table: the entries of a row must be contiguous")
+    return block_table.shape[1], block_table.stride(0) if B > 1 else block_table.shape[1]
+
+
+def _one_device(tensors):
+    """All given tensors on one device; its index."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _on_device(device, ws=None):
+    """Makes the tensors' device current for a call (the library launches on the current device)."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {device}")
+    if ws is not None and ws.device != device:
+        raise ValueError(f"workspace on {ws.device}, tensors on {device}")
+    return torch.cuda.device(device)
+
+
+def block_table_args(len, n_new, free_blocks, block_table, slots, start, len_out, info, block_size, free_pos=None):
+    """len, n_new, len_out int32 [B], free_blocks int32 [n_free], block_table
+    int32 [B, max_blocks] (rows may lie apart), slots int64 [max_new], start
+    int32 [B+1], info int32 [2], free_pos optional int32 [1].  len_out may be
+    len, and info[:1] free_pos."""
+    B = len.shape[0]
+    max_blocks, ld = _need_table(block_table, B)
+    for t, what, n in ((len, "len", B), (n_new, "n_new", B), (len_out, "len_out", B), (free_blocks, "free_blocks", None),
+                       (start, "start", B + 1), (info, "info", 2)):
+        _need(t, what, torch.int32, n)
+    _need(slots, "slots", torch.int64, None)
+    if free_pos is not None:
+        _need(free_pos, "free_pos", torch.int32, 1)
+    a = BlockTableArgs(B=B, block_size=block_size, max_blocks=max_blocks, ld_table=ld, len=_ptr(len), n_new=_ptr(n_new),
+                       free_blocks=_ptr(free_blocks), n_free=free_blocks.shape[0], free_pos=_ptr(free_pos),
+                       block_table=_ptr(block_table), len_out=_ptr(len_out), start=_ptr(start), slots=_ptr(slots),
+                       max_new=slots.shape[0], info=_ptr(info))
+    a._tensors = (len, n_new, free_blocks, free_pos, block_table, len_out, start, slots, info)
+    a._device = _one_device(a._tensors)
+    return a
+
+
+def csa2_block_tables(args, ws, stream=None):
+    """Block tables, pool rows and lengths of one step (see csa2.h)."""
+    with _on_device(args._device, ws):
+        _check(load().csa2_block_tables(ctypes.byref(args), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+               "csa2_block_tables")
+
+
+def csa2_paged_rows(positions, block_table, rows, block_size, n_blocks, n_vis=None, stream=None):
+    """positions and rows int32 [B, Q, K] (may be one tensor), block_table
+    int32 [B, max_blocks], n_vis optional int32 [B, Q]: pool rows of the
+    positions, -1 where there is none."""
+    B, Q, K = positions.shape
+    max_blocks, ld = _need_table(block_table, B)
+    _need(positions, "positions", torch.int32, B, Q, K)
+    _need(rows, "rows", torch.int32, B, Q, K)
+    if n_vis is not None:
+        _need(n_vis, "n_vis", torch.int32, B, Q)
+    a = PagedRowsArgs(B=B, Q=Q, K=K, block_size=block_size, max_blocks=max_blocks, ld_table=ld, n_blocks=n_blocks,
+                      positions=_ptr(positions), n_vis=_ptr(n_vis), block_table=_ptr(block_table), rows=_ptr(rows))
+    with _on_device(_one_device((positions, block_table, rows, n_vis))):
+        _check(load().csa2_paged_rows(ctypes.byref(a), _stream(stream)), "csa2_paged_rows")
+
+
+def paged_attn_args(q, kv, block_table, n_vis, out, lse=None, swa=None, W=0, swa_step=0, swa_scale=None, scale=0.0):
+    """q, out bf16 [B, Q, 64, 512]; kv the pool: uint8 [n_blocks, block_size,
+    288] FP4 entries or bf16 [n_blocks, block_size, 512] (blocks may lie
+    apart); block_table int32 [B, max_blocks]; n_vis int32 [B, Q]; lse f32
+    [B, Q, 64]; swa, W, swa_step, swa_scale as in attn_args."""
+    B, Q = q.shape[0], q.shape[1]
+    max_blocks, ld = _need_table(block_table, B)
+    _need(q, "q", torch.bfloat16, None, None, 64, 512)
+    _need(out, "out", torch.bfloat16, B, Q, 64, 512)
+    _need(n_vis, "n_vis", torch.int32, B, Q)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, B, Q, 64)
+    fp4 = kv.dtype == torch.uint8
+    width = ENTRY_BYTES if fp4 else 512
+    if kv.dim() != 3 or kv.shape[2] != width or (not fp4 and kv.dtype != torch.bfloat16) or kv.stride(2) != 1 or \
+            (kv.shape[1] > 1 and kv.stride(1) != width):
+        raise ValueError(f"kv: expected uint8 [n_blocks, block_size, 288] or bf16 [n_blocks, block_size, 512] with dense "
+                         f"blocks, got {kv.dtype} {list(kv.shape)} strides {kv.stride()}")
+    if W:
+        if swa is None:
+            raise ValueError("swa is needed for W > 0")
+        _need(swa, "swa", torch.bfloat16 if swa_scale is None else torch.uint8, B, None, 512)
+        if swa_scale is not None:
+            _need(swa_scale, "swa_scale", torch.float32, B, swa.shape[1])
+    stride = kv.stride(0) if kv.shape[0] > 1 else kv.shape[1] * width
+    a = PagedAttnArgs(B=B, Q=Q, W=W, block_size=kv.shape[1], max_blocks=max_blocks, ld_table=ld, n_blocks=kv.shape[0],
+                      block_stride=stride * kv.element_size(), q=_ptr(q), kv=_ptr(kv),
+                      kv_format=FMT_NVFP4 if fp4 else FMT_BF16, block_table=_ptr(block_table), n_vis=_ptr(n_vis),
+                      swa=_ptr(swa), swa_rows=swa.shape[1] if swa is not None else 0, swa_step=swa_step,
+                      swa_format=FMT_FP8 if swa_scale is not None else FMT_BF16, swa_scale=_ptr(swa_scale), scale=scale,
+                      out=_ptr(out), lse=_ptr(lse))
+    a._tensors = (q, kv, block_table, n_vis, swa, swa_scale, out, lse)     # the struct holds raw pointers
+    a._device = _one_device(a._tensors)
+    return a
+
+
+def csa2_paged_attn(args, ws, stream=None):
+    """Attention over all visible entries of a paged cache (see csa2.h)."""
+    with _on_device(args._device, ws):
+        _check(load().csa2_paged_attn(ctypes.byref(args), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+               "csa2_paged_attn")
 
 
 def csa2_workspace_size(args, which):

@@ -17,6 +17,8 @@
 #include "topk.cuh"
 #include "attention.cuh"
 #include "attention_tc.cuh"
+#include "paged_tables.cuh"
+#include "paged_attention.cuh"
 
 namespace csa2 {
 namespace {
@@ -162,7 +164,11 @@ csa2_status device_info(DeviceInfo** out) {
         set_smem_attrs(quantize_kv_fp4_kernel, 0) != cudaSuccess ||
         set_smem_attrs(quantize_window_fp8_kernel, 0) != cudaSuccess ||
         set_smem_attrs(quantize_index_k_mxfp4_kernel, 0) != cudaSuccess ||
-        set_smem_attrs(compress_rope_quantize_kernel, 0) != cudaSuccess)
+        set_smem_attrs(compress_rope_quantize_kernel, 0) != cudaSuccess ||
+        set_smem_attrs(block_tables_kernel, 0) != cudaSuccess || set_smem_attrs(block_rows_kernel, 0) != cudaSuccess ||
+        set_smem_attrs(paged_rows_kernel, 0) != cudaSuccess ||
+        set_smem_attrs(paged_attn_kernel, static_cast<int>(kPagedSmem)) != cudaSuccess ||
+        set_smem_attrs(paged_attn_join_kernel, 0) != cudaSuccess)
       return CSA2_ERR_CUDA;
     d.topk_max_cluster = topk_cluster_limit();
     if (!g_encode) {
@@ -549,6 +555,159 @@ csa2_status run_attn(const csa2_attn_args* a, void* ws, cudaStream_t st, bool ea
   trace_post(st);
   if (e2 != cudaSuccess) return CSA2_ERR_CUDA;
   return CSA2_OK;
+}
+
+// ---------------------------------------------------------------- paged cache
+csa2_status validate_table(int32_t block_size, int32_t max_blocks, int64_t ld_table) {
+  if (block_size < 1 || max_blocks < 1 || ld_table < max_blocks ||
+      static_cast<int64_t>(block_size) * max_blocks > CSA2_MAX_ENTRIES)
+    return CSA2_ERR_SHAPE;
+  return CSA2_OK;
+}
+
+csa2_status validate_block_tables(const csa2_block_table_args* a) {
+  if (!a) return CSA2_ERR_ARG;
+  if (a->B < 1 || a->B > CSA2_MAX_BQ || a->n_free < 0 || a->max_new < 0 || a->max_new > INT32_MAX) return CSA2_ERR_SHAPE;
+  const csa2_status s = validate_table(a->block_size, a->max_blocks, a->ld_table);
+  if (s != CSA2_OK) return s;
+  if (!a->len || !a->n_new || !a->block_table || !a->len_out || !a->start || !a->info ||
+      (a->n_free > 0 && !a->free_blocks) || (a->max_new > 0 && !a->slots))
+    return CSA2_ERR_ARG;
+  if (!aligned16(a->len) || !aligned16(a->n_new) || !aligned16(a->block_table) || !aligned16(a->len_out) ||
+      !aligned16(a->start) || !aligned16(a->info) || !aligned16(a->free_blocks) || !aligned16(a->slots) ||
+      !aligned16(a->free_pos))
+    return CSA2_ERR_ALIGN;
+  return CSA2_OK;
+}
+
+size_t block_tables_ws_bytes(const csa2_block_table_args* a) { return up256(static_cast<size_t>(a->B) * 4); }
+
+csa2_status run_block_tables(const csa2_block_table_args* a, void* ws, cudaStream_t st) {
+  TablesParams t;
+  t.B = a->B;
+  t.P = static_cast<uint32_t>(a->block_size);
+  t.cap = static_cast<int64_t>(a->block_size) * a->max_blocks;
+  t.ld_table = a->ld_table;
+  t.len = a->len; t.n_new = a->n_new; t.free_blocks = a->free_blocks; t.n_free = a->n_free; t.free_pos = a->free_pos;
+  t.table = a->block_table; t.len_out = a->len_out; t.start = a->start; t.slots = a->slots; t.max_new = a->max_new;
+  t.info = a->info;
+  t.base = static_cast<int32_t*>(ws);
+  const int fill = a->max_new <= kTablesOneLaunch ? 1 : 0;
+  trace_pre(kKBlockTables, st);
+  cudaError_t e = launch_ex(block_tables_kernel, dim3(1), dim3(kTablesThreads), 0, st, 0, t, fill);
+  trace_post(st);
+  if (e != cudaSuccess) return CSA2_ERR_CUDA;
+  if (fill) return CSA2_OK;
+  trace_pre(kKBlockRows, st);
+  e = launch_ex(block_rows_kernel, dim3(static_cast<unsigned>((a->max_new + kRowsPerBlock - 1) / kRowsPerBlock)),
+                dim3(kRowsPerBlock), 0, st, 0, t);
+  trace_post(st);
+  return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+csa2_status validate_paged_rows(const csa2_paged_rows_args* a) {
+  if (!a) return CSA2_ERR_ARG;
+  if (a->B < 1 || a->Q < 1 || static_cast<int64_t>(a->B) * a->Q > CSA2_MAX_BQ || a->K < 1 ||
+      static_cast<int64_t>(a->B) * a->Q * a->K > INT32_MAX || a->n_blocks < 1 || a->n_blocks > INT32_MAX)
+    return CSA2_ERR_SHAPE;
+  const csa2_status s = validate_table(a->block_size, a->max_blocks, a->ld_table);
+  if (s != CSA2_OK) return s;
+  if (a->n_blocks * a->block_size > INT32_MAX) return CSA2_ERR_SHAPE;
+  if (!a->positions || !a->block_table || !a->rows) return CSA2_ERR_ARG;
+  if (!aligned16(a->positions) || !aligned16(a->n_vis) || !aligned16(a->block_table) || !aligned16(a->rows))
+    return CSA2_ERR_ALIGN;
+  return CSA2_OK;
+}
+
+csa2_status run_paged_rows(const csa2_paged_rows_args* a, cudaStream_t st) {
+  PagedRowsParams p;
+  p.pos = a->positions; p.n_vis = a->n_vis; p.table = a->block_table; p.rows = a->rows;
+  p.n = static_cast<uint32_t>(a->B) * a->Q * a->K;
+  p.K = a->K; p.Q = a->Q; p.P = a->block_size;
+  p.max_blocks = a->max_blocks; p.n_blocks = static_cast<uint32_t>(a->n_blocks);
+  p.ld_table = a->ld_table;
+  trace_pre(kKPagedRows, st);
+  const cudaError_t e = launch_ex(paged_rows_kernel, dim3((p.n + 1023u) / 1024u), dim3(256), 0, st, 0, p);
+  trace_post(st);
+  return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+csa2_status validate_paged_attn(const csa2_paged_attn_args* a) {
+  if (!a) return CSA2_ERR_ARG;
+  if (a->B < 1 || a->Q < 1 || static_cast<int64_t>(a->B) * a->Q > CSA2_MAX_BQ || a->W < 0 || a->W > CSA2_MAX_W ||
+      a->n_blocks < 1 || a->n_blocks > INT32_MAX || a->swa_step < 0)
+    return CSA2_ERR_SHAPE;
+  csa2_status s = validate_table(a->block_size, a->max_blocks, a->ld_table);
+  if (s != CSA2_OK) return s;
+  if (a->kv_format != CSA2_FMT_NVFP4 && a->kv_format != CSA2_FMT_BF16) return CSA2_ERR_ARG;
+  if (a->swa_format != CSA2_FMT_BF16 && a->swa_format != CSA2_FMT_FP8) return CSA2_ERR_ARG;
+  const int64_t row_bytes = a->kv_format == CSA2_FMT_BF16 ? 1024 : CSA2_ENTRY_BYTES;
+  if (a->block_stride < row_bytes * a->block_size) return CSA2_ERR_SHAPE;
+  if (!a->q || !a->kv || !a->block_table || !a->n_vis || !a->out || (a->W > 0 && !a->swa) ||
+      (a->W > 0 && a->swa_format == CSA2_FMT_FP8 && !a->swa_scale))
+    return CSA2_ERR_ARG;
+  if (a->W > 0 && static_cast<int64_t>(a->Q - 1) * a->swa_step + a->W > a->swa_rows) return CSA2_ERR_SHAPE;
+  if ((a->block_stride & 15) || !aligned16(a->q) || !aligned16(a->kv) || !aligned16(a->block_table) ||
+      !aligned16(a->n_vis) || !aligned16(a->swa) || !aligned16(a->out) || !aligned16(a->lse) ||
+      (reinterpret_cast<uintptr_t>(a->swa_scale) & 3))
+    return CSA2_ERR_ALIGN;
+  return CSA2_OK;
+}
+
+// CTAs of the attention launch: one per SM, and no more than the tiles that
+// full tables would give.
+int paged_ctas(const csa2_paged_attn_args* a) {
+  const int64_t cap = static_cast<int64_t>(a->block_size) * a->max_blocks;
+  const int64_t tiles = std::max<int64_t>(1, (cap + kPagedKeys - 1) / kPagedKeys + (a->W + kPagedKeys - 1) / kPagedKeys);
+  return static_cast<int>(std::min<int64_t>(kPagedMaxCtas, tiles * a->B * a->Q));
+}
+
+struct PagedWs { size_t opart, ml, first, total; };
+PagedWs paged_ws(const csa2_paged_attn_args* a) {
+  const size_t n = paged_ctas(a);
+  PagedWs w;
+  w.opart = 0;
+  w.ml = w.opart + 2 * n * 64 * 512 * 4;
+  w.first = w.ml + 2 * n * 64 * 2 * 4;
+  w.total = up256(w.first + n * 4);
+  return w;
+}
+
+csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev, void* ws, cudaStream_t st) {
+  const float scale = a->scale > 0.0f ? a->scale : 1.0f / sqrtf(512.0f);
+  const PagedWs w = paged_ws(a);
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  PagedAttnParams p;
+  p.BQ = a->B * a->Q; p.Q = a->Q; p.W = a->W;
+  p.w_tiles = (a->W + kPagedKeys - 1) / kPagedKeys;
+  p.block_size = a->block_size; p.max_blocks = a->max_blocks;
+  p.ld_table = a->ld_table; p.n_blocks = a->n_blocks; p.block_stride = a->block_stride;
+  p.kv = static_cast<const uint8_t*>(a->kv);
+  p.kv_bf16 = a->kv_format == CSA2_FMT_BF16 ? 1 : 0;
+  p.table = a->block_table; p.n_vis = a->n_vis;
+  p.swa = static_cast<const uint8_t*>(a->swa);
+  p.swa_scale = a->swa_scale;
+  p.swa_fp8 = (a->W > 0 && a->swa_format == CSA2_FMT_FP8) ? 1 : 0;
+  p.swa_rows = a->swa_rows; p.swa_step = a->swa_step;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(a->out);
+  p.lse = a->lse;
+  p.opart = reinterpret_cast<float*>(wb + w.opart);
+  p.ml = reinterpret_cast<float*>(wb + w.ml);
+  p.first_row = reinterpret_cast<int32_t*>(wb + w.first);
+  CUtensorMap tq;
+  if (!make_map_bf16_512(&tq, a->q, static_cast<uint64_t>(p.BQ) * 64, 64)) return CSA2_ERR_CUDA;
+  const int ctas = std::min(paged_ctas(a), dev.sms);
+  trace_pre(kKPagedAttn, st);
+  cudaError_t e = launch_ex(paged_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPagedThreads), kPagedSmem, st, 0,
+                            tq, p);
+  trace_post(st);
+  if (e != cudaSuccess) return CSA2_ERR_CUDA;
+  if (ctas == 1) return CSA2_OK;                       // no range boundary
+  trace_pre(kKPagedJoin, st);
+  e = launch_ex(paged_attn_join_kernel, dim3(64, static_cast<unsigned>(ctas - 1)), dim3(128), 0, st, 0, p, ctas);
+  trace_post(st);
+  return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------- group call
@@ -1042,6 +1201,35 @@ csa2_status csa2_stack_decode_io(const csa2_stack_args* sa, const csa2_io* io, v
   return s != CSA2_OK ? s : e;
 }
 
+csa2_status csa2_block_tables(const csa2_block_table_args* a, void* ws, size_t ws_bytes, void* stream) {
+  csa2_status s = validate_block_tables(a);
+  if (s != CSA2_OK) return s;
+  if (!ws || ws_bytes < block_tables_ws_bytes(a) || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  s = device_info(&dev);
+  if (s != CSA2_OK) return s;
+  return run_block_tables(a, ws, static_cast<cudaStream_t>(stream));
+}
+
+csa2_status csa2_paged_rows(const csa2_paged_rows_args* a, void* stream) {
+  csa2_status s = validate_paged_rows(a);
+  if (s != CSA2_OK) return s;
+  DeviceInfo* dev = nullptr;
+  s = device_info(&dev);
+  if (s != CSA2_OK) return s;
+  return run_paged_rows(a, static_cast<cudaStream_t>(stream));
+}
+
+csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
+  csa2_status s = validate_paged_attn(a);
+  if (s != CSA2_OK) return s;
+  if (!ws || ws_bytes < paged_ws(a).total || !aligned16(ws)) return CSA2_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  s = device_info(&dev);
+  if (s != CSA2_OK) return s;
+  return run_paged_attn(a, *dev, ws, static_cast<cudaStream_t>(stream));
+}
+
 size_t csa2_noalloc_scratch_bytes(void) { return kNoAllocScratchBytes; }
 
 size_t csa2_workspace_size(const void* args, int32_t which) {
@@ -1061,6 +1249,14 @@ size_t csa2_workspace_size(const void* args, int32_t which) {
   if (which == CSA2_WS_STACK) {
     size_t need = 0;
     return validate_stack(static_cast<const csa2_stack_args*>(args), &need) == CSA2_OK ? need : 0;
+  }
+  if (which == CSA2_WS_PAGED_ATTN) {
+    const csa2_paged_attn_args* a = static_cast<const csa2_paged_attn_args*>(args);
+    return validate_paged_attn(a) == CSA2_OK ? paged_ws(a).total : 0;
+  }
+  if (which == CSA2_WS_BLOCK_TABLES) {
+    const csa2_block_table_args* a = static_cast<const csa2_block_table_args*>(args);
+    return validate_block_tables(a) == CSA2_OK ? block_tables_ws_bytes(a) : 0;
   }
   return 0;
 }
@@ -1155,6 +1351,11 @@ const char* csa2_kernel_name(int32_t kernel) {
     case kKQuantizeWindow: return "quantize_window_fp8_kernel";
     case kKQuantizeIndexK: return "quantize_index_k_mxfp4_kernel";
     case kKCompressRope: return "compress_rope_quantize_kernel";
+    case kKBlockTables: return "block_tables_kernel";
+    case kKBlockRows: return "block_rows_kernel";
+    case kKPagedRows: return "paged_rows_kernel";
+    case kKPagedAttn: return "paged_attn_kernel";
+    case kKPagedJoin: return "paged_attn_join_kernel";
     default: return "unknown";
   }
 }

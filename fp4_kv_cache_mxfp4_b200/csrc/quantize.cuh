@@ -106,6 +106,7 @@ quantize_kv_fp4_kernel(const __nv_bfloat16* __restrict__ x, int64_t n, int64_t l
   uint32_t s_code;
   fp4_block16_bf16(v, nib, s_code);                   // bf16 inputs: one division per block
   const int64_t dst = dst_rows ? dst_rows[row] : row_offset + row;
+  if (dst < 0) return;                                // an entry without a place
   uint8_t* out = kv + dst * 288;
   *reinterpret_cast<uint2*>(out + lane * 8) = nib;
   out[256 + lane] = static_cast<uint8_t>(s_code);
@@ -174,6 +175,7 @@ quantize_window_fp8_kernel(const __nv_bfloat16* __restrict__ x, int64_t n, int64
     w[k] = word;
   }
   const int64_t dst = dst_rows ? dst_rows[row] : row_offset + row;
+  if (dst < 0) return;                                // an entry without a place
   *reinterpret_cast<uint4*>(codes + dst * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   if (lane == 0) scales[dst] = s;
 }
@@ -233,6 +235,7 @@ quantize_index_k_mxfp4_kernel(const __nv_bfloat16* __restrict__ x, int64_t n, in
     nib |= byte << (8 * i);
   }
   const int64_t dst = dst_rows ? dst_rows[row] : row_offset + row;
+  if (dst < 0) return;                                // an entry without a place
   uint8_t* entry = out + dst * 68;
   *reinterpret_cast<uint16_t*>(entry + 2 * lane) = static_cast<uint16_t>(nib);
   if ((lane & 7) == 0) entry[64 + (lane >> 3)] = static_cast<uint8_t>(e + 127);
@@ -309,6 +312,7 @@ compress_rope_quantize_kernel(const __nv_bfloat16* __restrict__ x, int64_t n, in
   uint32_t s_code;
   fp4_block16(v, nib, s_code);
   const int64_t dst = dst_rows ? dst_rows[e] : row_offset + e;
+  if (dst < 0) return;                                // an entry without a place
   uint8_t* out = kv + dst * 288;
   *reinterpret_cast<uint2*>(out + lane * 8) = nib;
   out[256 + lane] = static_cast<uint8_t>(s_code);

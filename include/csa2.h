@@ -61,6 +61,7 @@ extern "C" {
 #define CSA2_MAX_BQ       65535 /* batch rows x query positions per call      */
 #define CSA2_MAX_K        2048  /* largest top-K (and largest pool, in blocks) */
 #define CSA2_MAX_W        1024  /* largest window (rows per query)            */
+#define CSA2_MAX_ENTRIES  (1 << 30) /* entries that one block-table row names */
 
 typedef enum csa2_status {
     CSA2_OK            = 0,
@@ -104,8 +105,9 @@ typedef enum csa2_mode {
  *             and a multiple of 8
  *   n         entries, >= 0 (0 enqueues nothing)
  *   kv_fp4    u8 cache rows of CSA2_ENTRY_BYTES bytes
- *   dst_rows  optional int64 [n]: entry i goes to row dst_rows[i];
- *             NULL means row row_offset + i
+ *   dst_rows  optional int64 [n]: entry i goes to row dst_rows[i], or
+ *             nowhere when that is negative (the padding of
+ *             csa2_block_tables); NULL means row row_offset + i
  *   row_offset  first destination row when dst_rows is NULL, >= 0
  * Entries map to distinct rows (overlapping destinations race).  The call
  * does not know the cache's size: every destination row must lie inside
@@ -493,8 +495,137 @@ csa2_status csa2_group_decode_io(const csa2_group_args* g, const csa2_io* io, vo
 csa2_status csa2_stack_decode_io(const csa2_stack_args* s, const csa2_io* io, void* ws,
                                  size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache.  (The pages have no counterpart: this serves programs
+ * that keep the caches of many requests in one pool.)
+ *
+ * The pool is an array of blocks of block_size entries each; row
+ * id * block_size + i of the pool is entry i of block id.  A request's
+ * entries 0, 1, ... lie in the blocks that its row of the block table names:
+ * entry e in block block_table[b][e / block_size].  The table's rows are
+ * ld_table int32 apart, max_blocks of them in use;
+ * max_blocks * block_size <= CSA2_MAX_ENTRIES.
+ *
+ * csa2_block_tables -- one step's bookkeeping from request lengths, all on
+ * the device (a captured call serves growing lengths).  Request b holds
+ * len[b] entries and gets n_new[b] more.  It takes
+ *     ceil((len + n_new) / block_size) - ceil(len / block_size)
+ * blocks, in request order, from free_blocks[free_pos .. n_free), which are
+ * written to its table row behind those it has; the rows of its new entries
+ * follow those of request b - 1 in `slots`, the list that the cache writers
+ * take as dst_rows.
+ *   start[b]     first index of request b's entries in slots; start[B] their
+ *                number
+ *   slots[i]     pool row of new entry i; -1 for i >= start[B] (a padded
+ *                batch) and for the entries of a refused request
+ *   len_out[b]   len[b] + n_new[b], or len[b] of a refused request; may be
+ *                the array len itself
+ *   info[0]      index of the first block still free; may be free_pos
+ *                itself
+ *   info[1]      requests refused
+ * A request is refused, and takes nothing, when len or n_new is negative,
+ * its entries would pass max_blocks * block_size, its rows would pass
+ * max_new, or its blocks would pass n_free (then every later request that
+ * needs a block is refused too; requests that fit in the block they have
+ * are served).  A refused request's rows keep their place in slots; the
+ * start indices end at max_new.  Table entries of other blocks stay as they
+ * are.  Block ids are passed on as given.
+ * ---------------------------------------------------------------------- */
+typedef struct csa2_block_table_args {
+    int32_t        B;           /* requests, 1..CSA2_MAX_BQ                      */
+    int32_t        block_size;  /* entries per block, >= 1                       */
+    int32_t        max_blocks;  /* blocks per table row, >= 1                    */
+    int64_t        ld_table;    /* >= max_blocks                                 */
+    const int32_t* len;         /* int32 [B]                                     */
+    const int32_t* n_new;       /* int32 [B]                                     */
+    const int32_t* free_blocks; /* int32 [n_free] (may be NULL when n_free is 0) */
+    int32_t        n_free;
+    const int32_t* free_pos;    /* optional int32 [1]; NULL means 0              */
+    int32_t*       block_table; /* in/out int32 [B][ld_table]                    */
+    int32_t*       len_out;     /* out int32 [B]                                 */
+    int32_t*       start;       /* out int32 [B + 1]                             */
+    int64_t*       slots;       /* out int64 [max_new]                           */
+    int64_t        max_new;     /* 0 .. 2^31 - 1 (slots may be NULL when 0)      */
+    int32_t*       info;        /* out int32 [2]                                 */
+} csa2_block_table_args;
+
+csa2_status csa2_block_tables(const csa2_block_table_args* a, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * csa2_paged_rows -- pool rows of selected positions: what turns the indices
+ * of csa2_index_score_topk (entry positions of a request) into the indices
+ * of csa2_sparse_attn over the pool (B = 1, Q = all queries, N = n_blocks *
+ * block_size).
+ *     rows[b][q][k] = block_table[b][pos / block_size] * block_size
+ *                     + pos % block_size
+ * or -1 where pos is negative, at or beyond n_vis[b][q] (or the table's
+ * end), or the table names no block of the pool.  rows may be positions.
+ * ---------------------------------------------------------------------- */
+typedef struct csa2_paged_rows_args {
+    int32_t        B, Q;        /* B * Q <= CSA2_MAX_BQ                          */
+    int32_t        K;           /* positions per query, >= 1; B * Q * K < 2^31   */
+    int32_t        block_size, max_blocks;
+    int64_t        ld_table;
+    int64_t        n_blocks;    /* blocks in the pool; n_blocks * block_size < 2^31 */
+    const int32_t* positions;   /* int32 [B][Q][K]                               */
+    const int32_t* n_vis;       /* optional int32 [B][Q]                         */
+    const int32_t* block_table; /* int32 [B][ld_table]                           */
+    int32_t*       rows;        /* out int32 [B][Q][K]                           */
+} csa2_paged_rows_args;
+
+csa2_status csa2_paged_rows(const csa2_paged_rows_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * csa2_paged_attn -- the attention of csa2_sparse_attn over ALL of a query's
+ * visible entries in a paged cache instead of a selection: contexts that the
+ * top-K would select whole, and layers without an indexer.
+ *
+ * Query (b,q) attends to entries [0, n_vis[b][q]) of request b, followed by
+ * the window rows swa[b][q*swa_step + r], r in [0, W); key = value, one
+ * softmax; out, lse, scale and the window's formats as in csa2_sparse_attn.
+ * n_vis outside [0, max_blocks * block_size] is taken as the nearest bound.
+ * Entries in a block that the table does not name (an id outside
+ * [0, n_blocks)) are no keys; rows of the pool that no visible entry lies in
+ * are not read, whatever they hold.  A query with no key gets out = 0 and
+ * lse = -inf.
+ *
+ * kv_format CSA2_FMT_NVFP4: pool rows are 288-byte FP4 entries
+ * (csa2_quantize_kv_fp4); CSA2_FMT_BF16: 512 bf16 values.  Blocks lie
+ * block_stride bytes apart (>= block_size rows, a multiple of 16; more when
+ * several layers' blocks share one pool); the rows of a block are dense.
+ *
+ * The keys of all queries together are cut into equal pieces, one per SM,
+ * whatever the lengths; queries that a cut divides are joined from fp32
+ * partials in the workspace, always in the same order.
+ * ---------------------------------------------------------------------- */
+typedef struct csa2_paged_attn_args {
+    int32_t        B, Q;        /* B * Q <= CSA2_MAX_BQ                          */
+    int32_t        W;           /* window rows per query, 0..CSA2_MAX_W          */
+    int32_t        block_size, max_blocks;
+    int64_t        ld_table;
+    int64_t        n_blocks;    /* blocks in the pool, 1 .. 2^31 - 1             */
+    int64_t        block_stride;/* bytes                                         */
+    const void*    q;           /* bf16 [B][Q][64][512]                          */
+    const void*    kv;          /* the pool                                      */
+    int32_t        kv_format;   /* CSA2_FMT_NVFP4 or CSA2_FMT_BF16               */
+    const int32_t* block_table; /* int32 [B][ld_table]                           */
+    const int32_t* n_vis;       /* int32 [B][Q]                                  */
+    const void*    swa;         /* W > 0: window rows, as in csa2_attn_args      */
+    int32_t        swa_rows, swa_step;
+    int32_t        swa_format;  /* CSA2_FMT_BF16 or CSA2_FMT_FP8                 */
+    const float*   swa_scale;   /* CSA2_FMT_FP8: f32 [B][swa_rows]               */
+    float          scale;       /* logit scale; <= 0 means 1/sqrt(512)           */
+    void*          out;         /* out bf16 [B][Q][64][512]                      */
+    float*         lse;         /* optional out f32 [B][Q][64]                   */
+} csa2_paged_attn_args;
+
+csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* ws,
+                            size_t ws_bytes, void* stream);
+
 /* Workspace bytes needed by a call.  which = 1: csa2_index_args,
- * 2: csa2_attn_args, 3: csa2_group_args, 4: csa2_stack_args.  Returns 0
+ * 2: csa2_attn_args, 3: csa2_group_args, 4: csa2_stack_args,
+ * 5: csa2_paged_attn_args, 6: csa2_block_table_args.  Returns 0
  * when the arguments are invalid for that call.
  *
  * Launches: every kernel is launched with programmatic stream serialisation
@@ -506,6 +637,8 @@ csa2_status csa2_stack_decode_io(const csa2_stack_args* s, const csa2_io* io, vo
 #define CSA2_WS_ATTN  2
 #define CSA2_WS_GROUP 3
 #define CSA2_WS_STACK 4
+#define CSA2_WS_PAGED_ATTN 5
+#define CSA2_WS_BLOCK_TABLES 6
 size_t csa2_workspace_size(const void* args, int32_t which);
 
 /* Reads and clears the device-side failure word of the current device
@@ -549,6 +682,11 @@ int32_t csa2_version(void);
 #define CSA2_KERNEL_QUANTIZE_WINDOW 5
 #define CSA2_KERNEL_QUANTIZE_INDEX_K 6
 #define CSA2_KERNEL_COMPRESS_ROPE   7
+#define CSA2_KERNEL_BLOCK_TABLES 8
+#define CSA2_KERNEL_BLOCK_ROWS   9
+#define CSA2_KERNEL_PAGED_ROWS  10
+#define CSA2_KERNEL_PAGED_ATTN  11
+#define CSA2_KERNEL_PAGED_JOIN  12
 csa2_status csa2_trace_begin(int32_t max_launches);
 csa2_status csa2_trace_stop(void);
 csa2_status csa2_trace_end(void);
