@@ -167,7 +167,8 @@ csa2_status device_info(DeviceInfo** out) {
         set_smem_attrs(compress_rope_quantize_kernel, 0) != cudaSuccess ||
         set_smem_attrs(block_tables_kernel, 0) != cudaSuccess || set_smem_attrs(block_rows_kernel, 0) != cudaSuccess ||
         set_smem_attrs(paged_rows_kernel, 0) != cudaSuccess ||
-        set_smem_attrs(paged_attn_kernel, static_cast<int>(kPagedSmem)) != cudaSuccess ||
+        set_smem_attrs(paged_attn_kernel<false>, static_cast<int>(kPagedSmem)) != cudaSuccess ||
+        set_smem_attrs(paged_attn_kernel<true>, static_cast<int>(kPagedSmem)) != cudaSuccess ||
         set_smem_attrs(paged_attn_join_kernel, 0) != cudaSuccess)
       return CSA2_ERR_CUDA;
     d.topk_max_cluster = topk_cluster_limit();
@@ -683,7 +684,6 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   p.block_size = a->block_size; p.max_blocks = a->max_blocks;
   p.ld_table = a->ld_table; p.n_blocks = a->n_blocks; p.block_stride = a->block_stride;
   p.kv = static_cast<const uint8_t*>(a->kv);
-  p.kv_bf16 = a->kv_format == CSA2_FMT_BF16 ? 1 : 0;
   p.table = a->block_table; p.n_vis = a->n_vis;
   p.swa = static_cast<const uint8_t*>(a->swa);
   p.swa_scale = a->swa_scale;
@@ -699,13 +699,14 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   if (!make_map_bf16_512(&tq, a->q, static_cast<uint64_t>(p.BQ) * 64, 64)) return CSA2_ERR_CUDA;
   const int ctas = std::min(paged_ctas(a), dev.sms);
   trace_pre(kKPagedAttn, st);
-  cudaError_t e = launch_ex(paged_attn_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPagedThreads), kPagedSmem, st, 0,
-                            tq, p);
+  cudaError_t e = launch_ex(a->kv_format == CSA2_FMT_BF16 ? paged_attn_kernel<true> : paged_attn_kernel<false>,
+                            dim3(static_cast<unsigned>(ctas)), dim3(kPagedThreads), kPagedSmem, st, 0, tq, p);
   trace_post(st);
   if (e != cudaSuccess) return CSA2_ERR_CUDA;
   if (ctas == 1) return CSA2_OK;                       // no range boundary
   trace_pre(kKPagedJoin, st);
-  e = launch_ex(paged_attn_join_kernel, dim3(64, static_cast<unsigned>(ctas - 1)), dim3(128), 0, st, 0, p, ctas);
+  e = launch_ex(paged_attn_join_kernel, dim3(64, static_cast<unsigned>(std::min(p.BQ, ctas - 1))),
+                dim3(kPagedJoinThreads), 0, st, 0, p, ctas);
   trace_post(st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

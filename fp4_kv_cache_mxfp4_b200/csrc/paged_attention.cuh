@@ -17,17 +17,59 @@
 // A CTA has at most two partials: its first query (when that began in an
 // earlier range) and its last (when that goes on).
 //
-// Tile mathematics as in attention_tc.cuh: S^T[key, head] = K . Q^T
-// (M = 128 keys, N = 64), weights exp2(S^T - ref) in bf16 against a running
-// reference, O^T[dim, head] += V^T . P^T with the same key tile.
+// Mathematics of a tile, as in attention_tc.cuh: S^T[key, head] = K . Q^T
+// (tcgen05, M = 128 keys, N = 64 heads, K = 512 dims), weights
+// P^T = exp2(S^T - ref) in bf16 against a running reference per head that
+// moves only when a logit passes it by 2^8, O^T[dim, head] += V^T . P^T
+// (M = 128 dims x 4, N = 64, K = 128 keys) with the same bf16 key tile read
+// along its other axis.
+//
+// What bounds it: 64 MMA instructions per tile, each reading 6 KB of operands
+// from shared memory at 128 B per cycle, 48 cycles (measured), so 3072 cycles
+// per tile: 2.7 MMAC of a possible 4.1 per cycle.  One key tile (128 KB), Q (64 KB)
+// and P^T (16 KB) fill the shared memory, so the tile is filled in slabs of
+// 128 dims: MMA 2 releases slab t when its output rows t are done, and the
+// next tile's slab t is expanded while MMA 2 runs on the others.  Roles:
+//   warps 0-7    loaders: rows -> bf16 slabs (FP4 entries of the next tile
+//                wait in registers; bf16 rows go by cp.async)
+//   warps 8-23   softmax: S^T from tensor memory, weights to P^T, and the
+//                epilogue; warp w has keys 32 (w % 4).. and heads 16 (w / 4 - 2)..
+//   warp 24      MMA issue
+//   warp 25      row addresses of the tiles to come (block table, window),
+//                up to three tiles ahead, and their prefetch to L2
+//   warps 26-27  Q (TMA, then the channel order below)
+// Every role fits in the 72 registers that 28 warps leave each thread: with
+// the whole shared memory taken, L1 is too small for spilled values to stay,
+// and each reload then costs an L2 round trip (a version with some twenty
+// spilled registers took 1.5 times as long).
+//
+// FP4 to bf16 in 9 logic, 4 multiply-add and 4 half-precision instructions
+// per 8 channels (the ALU rate, half the FMA rate, is what bounds the
+// loaders; a table look-up by byte permutes takes 26 logic ones and made the
+// conversion of a tile 5600 cycles): the nibble pair (j, j + 4) of a word,
+// times 2^12 + 2^6, has each sign at bit 15 and each magnitude at bits 6..8
+// of its half, which read as bf16 is the value times 2^-126 (subnormals
+// included, as in E2M1).  One multiplication by scale * 2^118 leaves the
+// entry times 2^-8 (2^126 * 448 would overflow), exactly.  So in a pool of FP4 entries
+//   - every 16-byte unit of an operand holds channels 0 4 1 5 2 6 3 7 of its
+//     eight: Q and the window rows are permuted alike, and the epilogue
+//     writes each dim to its channel;
+//   - logits of cache tiles are multiplied by 2^8, weights of window keys by
+//     2^-8 and the result by 2^8.
 #pragma once
 #include "common.cuh"
 #include "quantize.cuh"
 #include "attention_tc.cuh"
+#include "paged_tables.cuh"
+#include "topk.cuh"
 
 namespace csa2 {
 
-constexpr int kPagedThreads = 512;
+constexpr int kPagedLoaders = 8, kPagedSoftmax = 16, kPagedQWarps = 2;      // warps
+constexpr int kPagedThreads = 32 * (kPagedLoaders + kPagedSoftmax + 2 + kPagedQWarps);
+constexpr int kPagedStages = 3;                        // tiles whose row addresses are kept
+constexpr int kPagedEndBar = 5;                         // named barriers: 1-4 the softmax quarters, 5 the end
+constexpr float kPagedFp4Up = 256.0f, kPagedFp4Down = 0.00390625f;
 constexpr int kPagedKeys = 128;                        // keys per tile (MMA M)
 constexpr int kPagedMaxCtas = 148;                     // one per SM of a B200
 constexpr uint32_t kPagedSmem = kTcAttnSmem;
@@ -38,7 +80,6 @@ struct PagedAttnParams {
   uint32_t block_size, max_blocks;
   int64_t ld_table, n_blocks, block_stride;            // block_stride in bytes
   const uint8_t* kv;
-  int kv_bf16;               // cache rows: 0 FP4 entries (288 B), 1 bf16 (1024 B)
   const int32_t* table;
   const int32_t* n_vis;      // [B][Q]
   const uint8_t* swa;        // bf16 rows or E4M3 codes
@@ -53,17 +94,16 @@ struct PagedAttnParams {
 };
 
 // Tiles of query r: at least one, so that a query without any key is written too.
-__device__ __forceinline__ int64_t paged_tiles(const PagedAttnParams& p, int r, int* keys) {
-  const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.block_size;
-  const int64_t n = min(static_cast<int64_t>(max(p.n_vis[r], 0)), cap);
-  *keys = static_cast<int>(n);
-  return max((n + kPagedKeys - 1) / kPagedKeys + p.w_tiles, static_cast<int64_t>(1));
+__device__ __forceinline__ int paged_tiles(const PagedAttnParams& p, int r, int* keys) {
+  // max_blocks * block_size <= 2^30
+  *keys = min(max(p.n_vis[r], 0), static_cast<int>(p.max_blocks * p.block_size));
+  return max((*keys + kPagedKeys - 1) / kPagedKeys + p.w_tiles, 1);
 }
 
 // This CTA's tile range [lo, hi) of the total, the query that lo lies in and
 // lo's offset inside it.  Every CTA sums the tiles of all queries (4 bytes
 // each from L2); every thread calls it.
-struct PagedRange { int64_t lo, hi; int row; int64_t offset; };
+struct PagedRange { int64_t lo, hi; int row, offset; };
 __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int64_t* warp_s, PagedRange* range_s) {
   const int per = (p.BQ + blockDim.x - 1) / blockDim.x;
   const int r0 = min(p.BQ, static_cast<int>(threadIdx.x) * per), r1 = min(p.BQ, r0 + per);
@@ -77,13 +117,40 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int6
   const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
   if (lo >= at && lo < at + mine) {
     for (int r = r0; r < r1; ++r) {
-      const int64_t t = paged_tiles(p, r, &keys);
-      if (lo < at + t) { *range_s = PagedRange{lo, hi, r, lo - at}; break; }
+      const int t = paged_tiles(p, r, &keys);
+      if (lo < at + t) { *range_s = PagedRange{lo, hi, r, static_cast<int>(lo - at)}; break; }
       at += t;
     }
   }
   __syncthreads();
   return *range_s;
+}
+
+// Walks the tiles of a CTA's range: tiles [t, t1) of query `row`, then the next query's.
+struct PagedCursor {
+  int64_t left;              // tiles of the range from tile t on
+  int t, t1, tiles;          // this tile, the end of the range's part of the query, the query's tiles
+  int row, keys, kv_tiles;
+};
+__device__ __forceinline__ void paged_enter(const PagedAttnParams& p, PagedCursor& c, int row, int offset) {
+  c.row = row;
+  c.tiles = paged_tiles(p, row, &c.keys);
+  c.kv_tiles = (c.keys + kPagedKeys - 1) / kPagedKeys;
+  c.t = offset;
+  c.t1 = static_cast<int>(min(static_cast<int64_t>(c.tiles), offset + c.left));
+}
+// The cursor at the range's first tile.
+__device__ __forceinline__ PagedCursor paged_begin(const PagedAttnParams& p, const volatile PagedRange* r) {
+  PagedCursor c;
+  c.left = r->hi - r->lo;
+  paged_enter(p, c, r->row, r->offset);
+  return c;
+}
+// To the next tile; false behind the last.
+__device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedCursor& c) {
+  if (--c.left <= 0) return false;
+  if (++c.t == c.t1) paged_enter(p, c, c.row + 1, 0);
+  return true;
 }
 
 // Address of entry `pos` of a request's cache; nullptr where the table names no block of the pool.
@@ -95,337 +162,703 @@ __device__ __forceinline__ const uint8_t* paged_row(const PagedAttnParams& p, co
   return p.kv + id * p.block_stride + static_cast<int64_t>(pos - blk * p.block_size) * row_bytes;
 }
 
+// Wait of a whole warp.  Every lane polls: with one lane polling for the
+// others, the warp could go on in two parts, and what all lanes must execute
+// together (tcgen05, named barriers) then happened twice.
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, int err, volatile int* abort) {
+  const bool ok = mbar_wait(bar, parity, err, abort);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ void paged_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  __syncwarp();
+}
+__device__ __forceinline__ void paged_bar(int id, int nthreads) {
+  __syncwarp();
+  named_bar_sync(id, nthreads);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void sts(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" :: "r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ void sts(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" :: "r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts(uint32_t a, const uint8_t* v) { asm volatile("st.shared.b64 [%0], %1;" :: "r"(a), "l"(v) : "memory"); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ int lds_i(uint32_t a) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ const uint8_t* lds_ptr(uint32_t a) {
+  const uint8_t* v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+// (volatile: stays before the barrier that it is meant to hide)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  __syncwarp();
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Barrier `id` over n threads that also ORs a predicate over them.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool pred) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(id), "r"(n), "r"(static_cast<uint32_t>(pred)) : "memory");
+  return r != 0;
+}
+
+// Eight natural-order bf16 channels to the order 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ uint4 paged_order(uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
+}
+// Channel (0..7) of position i of such a unit.
+__device__ __forceinline__ int paged_channel(int i) { return (i >> 1) + 4 * (i & 1); }
+
+// Two E4M3 scale codes (bytes 0, 1 of w) to bf16, times 2^118: bits of an
+// E4M3 code at the bottom of a bf16 read as its value times 2^-120.
+__device__ __forceinline__ __nv_bfloat162 paged_scales(uint32_t w) {
+  const uint32_t a = __byte_perm(w, 0u, 0x4140);
+  const uint32_t m = ((a & 0x007F007Fu) << 4) | ((a & 0x00800080u) << 8);
+  const __nv_bfloat162 up1 = __floats2bfloat162_rn(1.329227995784916e36f, 1.329227995784916e36f);   // 2^120
+  const __nv_bfloat162 up2 = __floats2bfloat162_rn(3.323069989462290e35f, 3.323069989462290e35f);   // 2^118
+  return __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&m), up1), up2);
+}
+// Eight E2M1 codes to the unit's eight bf16 values (order as above), times scale * 2^-126.
+__device__ __forceinline__ uint4 paged_expand8(uint32_t w, __nv_bfloat162 scale) {
+  const uint32_t h = w >> 8;
+  uint32_t o[4] = {(w & 0x000F000Fu) * 0x1040u, (w & 0x00F000F0u) * 0x0104u, (h & 0x000F000Fu) * 0x1040u,
+                   (h & 0x00F000F0u) * 0x0104u};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    o[j] &= 0x81C081C0u;
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[j]), scale);
+    o[j] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+constexpr int kPagedPool = 0, kPagedBf16 = 1, kPagedFp8 = 2;       // kinds of tiles: cache entries, window rows
+
+// Loader threads and keys.  FP4 entries: keys 16 w + 8 i + kk (i = 0, 1)
+// with kk from lane bits 1, 2 and 4 and the 16-byte unit of a 64-byte slab
+// piece from bits 0 and 3, so that 8 lanes of a store phase hit 8 different
+// bank groups of the swizzled tile and every global sector is used whole.
+// bf16 and FP8 rows: keys 16 w + 4 i + lane / 8 (i = 0..3), unit lane % 8.
+
+template <bool KVB>
 __global__ void __launch_bounds__(kPagedThreads, 1)
 paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p) {
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* kt = smem;
-  uint8_t* qt = smem + kTcKeyTileBytes;
-  uint8_t* pt = qt + kTcQTileBytes;
-  uint8_t* misc = pt + kTcPTileBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(misc);   // [0] Q TMA, [1] MMA 1 done, [2] MMA 2 done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 48);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 52);
-  int* rescale_flag = reinterpret_cast<int*>(misc + 56);
-  float* red_s = reinterpret_cast<float*>(misc + 576);
-  float* ref_s = reinterpret_cast<float*>(misc + 2624);
-  float* sum_s = reinterpret_cast<float*>(misc + 2880);
-  float* fac_s = reinterpret_cast<float*>(misc + 3136);
-  float* wsc_s = reinterpret_cast<float*>(misc + 3392);               // [128] FP8 window: row scale per key
-  const uint8_t** row_s = reinterpret_cast<const uint8_t**>(misc + 4096);   // [128] key addresses, null = no key
-  int64_t* warp_s = reinterpret_cast<int64_t*>(misc + 5632);          // [33]
-  PagedRange* range_s = reinterpret_cast<PagedRange*>(misc + 6016);
+  // The tiles and what is read per tile go by 32-bit shared addresses: the
+  // pointers below are generic (twice the registers, and slower accesses).
+  const uint32_t kt = smem_u32(smem);                   // key tile: 8 chunks of [128 keys][64 dims], 2 per slab
+  const uint32_t qt = kt + kTcKeyTileBytes;
+  const uint32_t pt = qt + kTcQTileBytes;
+  const uint32_t misc32 = pt + kTcPTileBytes;
+  uint8_t* misc = smem + kTcKeyTileBytes + kTcQTileBytes + kTcPTileBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
+  uint64_t* full = bars;                                // [4] slab filled (8 loader warps)
+  uint64_t* freed = bars + 4;                           // [4] slab read by MMA 2
+  uint64_t* q_full = bars + 8;
+  uint64_t* s_full = bars + 9;                          // MMA 1 done (and every MMA before it)
+  uint64_t* p_full = bars + 10;                         // P^T written, O^T rescaled (16 softmax warps)
+  uint64_t* o_full = bars + 11;                         // the query part's last MMA 2 done
+  uint64_t* q_tma = bars + 12;                          // Q arrived, in natural order (FP4 pools)
+  uint64_t* q_free = bars + 13;                         // the query part's last MMA 1 done
+  uint64_t* rows_full = bars + 14;                      // [3] row addresses written
+  uint64_t* rows_free = bars + 17;                      // [3] ... and the tile's last MMA 2 done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 164);
+  const uint32_t kind_s = misc32 + 176;                               // int [3]
+  float* red_s = reinterpret_cast<float*>(misc + 256);                // [4 quarters][64 heads]
+  const uint32_t nref_s = misc32 + 1280;                              // float [64] minus the reference; +inf before any key
+  const uint32_t fac_s = misc32 + 1536;                               // float [64] rescale factor, later 1 / sum
+  int64_t* warp_s = reinterpret_cast<int64_t*>(misc + 1792);          // [33]
+  PagedRange* range_s = reinterpret_cast<PagedRange*>(misc + 2064);
+  const uint32_t row_s = misc32 + 2304;                               // [3][128] row address, null: no such key
+  const uint32_t wsc_s = misc32 + 5376;                               // float [3][128] FP8 row scales
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kMmaWarp = kPagedLoaders + kPagedSoftmax;
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 4; ++i) { mbar_init(&full[i], kPagedLoaders); mbar_init(&freed[i], 1); }
+    mbar_init(q_full, KVB ? 1 : kPagedQWarps);
+    mbar_init(q_tma, 1);
+    mbar_init(q_free, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, kPagedSoftmax);
+    mbar_init(o_full, 1);
+    for (int i = 0; i < kPagedStages; ++i) { mbar_init(&rows_full[i], 1); mbar_init(&rows_free[i], 1); }
     *abort_flag = 0;
-    *rescale_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
-  if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+  if (warp == kMmaWarp) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
   pdl_launch_dependents();
   pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // (read by asm: only asm writes it, which a plain load might not be told)
+  const uint32_t tmem = lds_i(misc32 + 160);
   const PagedRange range = paged_range(p, warp_s, range_s);
   if (tid == 0) p.first_row[blockIdx.x] = (range.lo < range.hi && range.offset > 0) ? range.row : -1;
 
-  uint32_t ph_q = 0, ph_mma = 0;
-  int row = range.row;
-  int64_t offset = range.offset;
-  for (int64_t at = range.lo; at < range.hi; ++row) {
-    int keys;
-    const int64_t tiles = paged_tiles(p, row, &keys);
-    const int kv_tiles = (keys + kPagedKeys - 1) / kPagedKeys;
-    const int64_t t0 = offset, t1 = min(tiles, offset + (range.hi - at));
-    const int b = row / p.Q, qi = row - b * p.Q;
-    const int32_t* table = p.table + b * p.ld_table;
-    if (tid == 0) {
-      mbar_arrive_expect_tx(&bars[0], kTcQTileBytes);
-      const uint64_t pol = l2_policy_evict_last();
-      for (int c = 0; c < 8; ++c) tma_load_2d(qt + c * 8192, &tmap_q, &bars[0], 64 * c, row * 64, pol);
-    }
-    if (tid < 64) { ref_s[tid] = -INFINITY; sum_s[tid] = 0.0f; }
-    for (int64_t t = t0; t < t1; ++t) {
-      const bool window = t >= kv_tiles;
-      const int key0 = static_cast<int>((window ? t - kv_tiles : t) * kPagedKeys);
-      const int nkeys = max(0, min(kPagedKeys, (window ? p.W : keys) - key0));
-      const bool win8 = window && p.swa_fp8;
-      const bool bf16_rows = window ? !p.swa_fp8 : p.kv_bf16 != 0;
-      if (tid < kPagedKeys) {
-        const uint8_t* a = nullptr;
-        float s = 0.0f;
-        if (tid < nkeys) {
-          if (window) {
-            const int64_t r = static_cast<int64_t>(b) * p.swa_rows + qi * p.swa_step + key0 + tid;
-            a = p.swa + r * (p.swa_fp8 ? 512 : 1024);
-            if (p.swa_fp8) s = p.swa_scale[r];
-          } else {
-            a = paged_row(p, table, static_cast<uint32_t>(key0 + tid), p.kv_bf16 ? 1024 : 288);
+  // Every role walks the same tiles.  Waits are bounded; after one gave up
+  // the others return at once, and every role still walks to its end (the
+  // named barriers stay matched), without writing results.
+  if (range.lo < range.hi) {
+    if (warp < kPagedLoaders) {
+      // ------------------------------------------------------------ loaders
+      int64_t left = range_s->hi - range_s->lo;
+      const int kk = ((lane >> 1) & 3) | ((lane >> 2) & 4), u = (lane & 1) | ((lane >> 2) & 2);
+      uint4 raw[4][2];                                  // FP4: [slab][key] 32 channels ...
+      uint16_t rsc[4][2];                               // ... and their two scales
+      int kind;
+      auto fetch = [&](int stage) {                     // the tile's kind and, of cache entries, their bytes
+        kind = lds_i(kind_s + 4 * stage);
+        if (!KVB && kind == kPagedPool) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* row = lds_ptr(row_s + 8 * (stage * 128 + 16 * warp + 8 * i + kk));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              raw[t][i] = make_uint4(0, 0, 0, 0);
+              rsc[t][i] = 0;
+              if (row) {
+                raw[t][i] = __ldg(reinterpret_cast<const uint4*>(row + 64 * t + 16 * u));
+                rsc[t][i] = __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 8 * t + 2 * u));
+              }
+            }
           }
         }
-        row_s[tid] = a;
-        wsc_s[tid] = s;
-      }
-      __syncthreads();
-      // warp w loads keys 8w..8w+7; a key that is not there becomes zeros
-      if (bf16_rows) {
+      };
+      auto publish = [&](int t) {
+        fence_async_smem();
+        paged_arrive(&full[t]);
+      };
+      paged_wait(&rows_full[0], 0, kErrWaitOperand, abort_flag);
+      fetch(0);
+      int stage = 0;
+      uint32_t ph_rows = 0;
+      for (uint32_t ph = 1;; ph ^= 1) {                 // ph: MMA 2 of the tile before has released the slab
+        if (!KVB && kind == kPagedPool) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 8 * warp + j;
-          const uint4* src = reinterpret_cast<const uint4*>(row_s[r]);
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t chunk = kt + (2 * t + (u >> 1)) * 16384;
+            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int u = lane + 32 * h;
-            const uint4 v = src ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(kt + (u >> 3) * 16384 + sw128_off(r, u & 7)) = v;
+            for (int i = 0; i < 2; ++i) {
+              const __nv_bfloat162 sc = paged_scales(rsc[t][i]);
+              const __nv_bfloat162 s0 = __low2bfloat162(sc), s1 = __high2bfloat162(sc);
+              const uint32_t w[4] = {raw[t][i].x, raw[t][i].y, raw[t][i].z, raw[t][i].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                sts(chunk + sw128_off(16 * warp + 8 * i + kk, 4 * (u & 1) + q), paged_expand8(w[q], q < 2 ? s0 : s1));
+            }
+            publish(t);
+          }
+        } else if (KVB && kind == kPagedPool) {
+          const uint8_t* row[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) row[i] = lds_ptr(row_s + 8 * (stage * 128 + 16 * warp + 4 * i + (lane >> 3)));
+          auto copy = [&](int t) {
+            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint8_t* src = row[i] ? row[i] + 256 * t + 16 * (lane & 7) : p.kv;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                cp_async16(kt + (2 * t + h) * 16384 + sw128_off(16 * warp + 4 * i + (lane >> 3), lane & 7),
+                           src + (row[i] ? 128 * h : 0), row[i] != nullptr);
+            }
+            cp_async_commit();
+          };
+          copy(0);
+          copy(1);
+          copy(2);
+          cp_async_wait<2>();
+          publish(0);
+          copy(3);
+          cp_async_wait<2>();
+          publish(1);
+          cp_async_wait<1>();
+          publish(2);
+          cp_async_wait<0>();
+          publish(3);
+        } else {
+          // window rows, in the pool's channel order, half a slab's rows at a time
+          const bool fp8 = kind == kPagedFp8;
+#pragma unroll 1
+          for (int t = 0; t < 4; ++t) {
+            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
+#pragma unroll 1
+            for (int i = 0; i < 4; i += 2) {
+              const uint8_t* row[2];
+              uint4 x[2][2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                row[k] = lds_ptr(row_s + 8 * (stage * 128 + 16 * warp + 4 * (i + k) + (lane >> 3)));
+                x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
+                if (row[k]) {
+                  const uint4* src = reinterpret_cast<const uint4*>(row[k] + (fp8 ? 128 : 256) * t) + (lane & 7);
+                  x[k][0] = __ldg(src);
+                  if (!fp8) x[k][1] = __ldg(src + 8);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int r = 16 * warp + 4 * (i + k) + (lane >> 3);
+                uint4 lo = x[k][0], hi = x[k][1];
+                uint32_t at = 2 * t * 16384 + sw128_off(r, lane & 7), at2 = at + 16384;
+                if (fp8) {
+                  e4m3x4_to_bf16(x[k][0].x, lo.x, lo.y);
+                  e4m3x4_to_bf16(x[k][0].y, lo.z, lo.w);
+                  e4m3x4_to_bf16(x[k][0].z, hi.x, hi.y);
+                  e4m3x4_to_bf16(x[k][0].w, hi.z, hi.w);
+                  const uint32_t chunk = (2 * t + ((lane >> 2) & 1)) * 16384;
+                  at = chunk + sw128_off(r, 2 * (lane & 3));
+                  at2 = chunk + sw128_off(r, 2 * (lane & 3) + 1);
+                }
+                sts(kt + at, KVB ? lo : paged_order(lo));
+                sts(kt + at2, KVB ? hi : paged_order(hi));
+              }
+            }
+            publish(t);
           }
         }
-      } else if (win8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 8 * warp + j;
-          const uint4* src = reinterpret_cast<const uint4*>(row_s[r]);
-          const uint4 raw = src ? __ldg(src + lane) : make_uint4(0, 0, 0, 0);
-          uint32_t o[8];
-          e4m3x4_to_bf16(raw.x, o[0], o[1]);
-          e4m3x4_to_bf16(raw.y, o[2], o[3]);
-          e4m3x4_to_bf16(raw.z, o[4], o[5]);
-          e4m3x4_to_bf16(raw.w, o[6], o[7]);
-          uint8_t* chunk = kt + (lane >> 2) * 16384;
-          *reinterpret_cast<uint4*>(chunk + sw128_off(r, 2 * (lane & 3))) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(chunk + sw128_off(r, 2 * (lane & 3) + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-        }
-      } else {
-        // FP4: half a row (16 lanes x 16 nibble bytes) of two keys per load
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 8 * warp + 2 * j + (lane >> 4), c = lane & 15;
-          const uint8_t* src = row_s[r];
-          const uint4 nib = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t sc = src ? __ldg(reinterpret_cast<const uint16_t*>(src + 256) + c) : 0;
-          const float s0 = e4m3_code_to_float(sc & 0xFF), s1 = e4m3_code_to_float(sc >> 8);
-          const __nv_bfloat162 S0 = __floats2bfloat162_rn(s0, s0), S1 = __floats2bfloat162_rn(s1, s1);
-          uint32_t o[4][4];
-          e2m1x8_to_bf16(nib.x, S0, o[0]);
-          e2m1x8_to_bf16(nib.y, S0, o[1]);
-          e2m1x8_to_bf16(nib.z, S1, o[2]);
-          e2m1x8_to_bf16(nib.w, S1, o[3]);
-          uint8_t* chunk = kt + (c >> 1) * 16384;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<uint4*>(chunk + sw128_off(r, 4 * (c & 1) + u)) = make_uint4(o[u][0], o[u][1], o[u][2], o[u][3]);
-        }
+        if (--left <= 0) break;
+        if (++stage == kPagedStages) { stage = 0; ph_rows ^= 1; }
+        paged_wait(&rows_full[stage], ph_rows, kErrWaitOperand, abort_flag);
+        fetch(stage);                                   // behind the tile's last fence, which would wait for the loads
       }
-      fence_async_smem();
-      __syncthreads();
-
-      // S^T = K . Q^T
-      if (warp == 1 && lane == 0) {
-        if (mbar_wait(&bars[0], ph_q, kErrWaitOperand, abort_flag)) {
-          tc_fence_after();
-          constexpr uint32_t idesc = umma_idesc_bf16_f32(128, 64);
-          const uint32_t ka = smem_u32(kt), qa = smem_u32(qt);
+    } else if (warp < kMmaWarp) {
+      // ------------------------------------------------------------ softmax
+      PagedCursor c = paged_begin(p, range_s);
+      const int quarter = warp & 3, hg = (warp - kPagedLoaders) >> 2, bar = 1 + hg;
+      const int key = 32 * quarter + lane, head0 = 16 * hg;
+      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+      uint32_t ph_o = 0;
+      int stage = 0;
+      float sum[16];                                    // this key's weights, summed over the tiles, per head
+      bool first = true, part_begins = false;
+      for (uint32_t it = 0;; ++it) {
+        if (first) {
+          part_begins = c.t == 0;
+          if (quarter == 0 && lane < 16) sts(nref_s + 4 * (head0 + lane), INFINITY);
 #pragma unroll
-          for (int kk = 0; kk < 32; ++kk)
-            umma_bf16(tmem, umma_desc_sw128_kmajor(ka + (kk >> 2) * 16384 + (kk & 3) * 32),
-                      umma_desc_sw128_kmajor(qa + (kk >> 2) * 8192 + (kk & 3) * 32), idesc, kk > 0);
+          for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
+          paged_bar(bar, 128);
         }
-        umma_commit(&bars[1]);
-      }
-      const bool first = t == t0;
-      {
-        const int quarter = warp & 3, hg = warp >> 2;
-        const int key = quarter * 32 + lane;
-        float sv[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sv[j] = -INFINITY;
-        const bool ok = mbar_wait(&bars[1], ph_mma, kErrWaitTmemFull, abort_flag);
-        if (__all_sync(0xffffffffu, ok)) {
-          tc_fence_after();
-          const bool there = row_s[key] != nullptr;
-          const float ls = p.scale_log2 * (win8 ? wsc_s[key] : 1.0f);
+        const bool window = c.t >= c.kv_tiles;
+        paged_wait(&full[0], it & 1, kErrWaitSmemEmpty, abort_flag);      // the loaders have seen the tile's addresses
+        const bool there = lds_ptr(row_s + 8 * (stage * 128 + key)) != nullptr;
+        float rs = (window && p.swa_fp8) ? lds_f(wsc_s + 4 * (stage * 128 + key)) : 1.0f;
+        if (++stage == kPagedStages) stage = 0;
+        const float ls = p.scale_log2 * (KVB || window ? rs : kPagedFp4Up);
+        if (!KVB && window) rs *= kPagedFp4Down;
+        paged_wait(s_full, it & 1, kErrWaitTmemFull, abort_flag);
+        tc_fence_after();
+        // y = exp2(logit - reference) in log2 units; a head without a reference yet has +inf
+        float y[16];
+        float over = -INFINITY;
+        auto weights = [&]() {
           uint32_t r[16];
-          tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 16 * hg, r);
+          tmem_ld_32x32b_x16(tmem + lanes + head0, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) sv[j] = there ? __uint_as_float(r[j]) * ls : -INFINITY;
-        }
-        const float m = warp_reduce_heads16<true>(sv, lane);
-        if ((lane & 1) == 0) red_s[quarter * 64 + 16 * hg + (lane >> 1)] = m;
-        __syncthreads();
-        float lj[16];
+          for (int j = 0; j < 16; j += 4) {
+            const float4 nr = lds_f4(nref_s + 4 * (head0 + j));
+            y[j] = fmaf(__uint_as_float(r[j]), ls, nr.x);
+            y[j + 1] = fmaf(__uint_as_float(r[j + 1]), ls, nr.y);
+            y[j + 2] = fmaf(__uint_as_float(r[j + 2]), ls, nr.z);
+            y[j + 3] = fmaf(__uint_as_float(r[j + 3]), ls, nr.w);
+          }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int h = 16 * hg + j;
-          const float mt = fmaxf(fmaxf(red_s[h], red_s[64 + h]), fmaxf(red_s[128 + h], red_s[192 + h]));
-          const float ref = ref_s[h];
-          const float nref = (mt > ref + kTcRefSlack) ? mt : ref;
-          lj[j] = exp2f(sv[j] - ((nref == -INFINITY) ? 0.0f : nref));
+          for (int j = 0; j < 16; ++j) y[j] = there ? y[j] : -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            over = fmaxf(over, y[j]);
+            y[j] = ex2(y[j]);
+          }
+        };
+        weights();
+        if (named_bar_or(bar, 128, over > kTcRefSlack)) {
+          // some reference moves: the tile's maximum per head, over the lanes and the four quarters
+          {
+            float v[16];
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tmem + lanes + head0, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = there ? __uint_as_float(r[j]) * ls : -INFINITY;
+            const float m = warp_reduce_heads16<true>(v, lane);
+            if ((lane & 1) == 0) red_s[quarter * 64 + head0 + (lane >> 1)] = m;
+          }
+          paged_bar(bar, 128);
+          if (quarter == 0) {                           // every lane, so that the warp stays together; 16 write
+            const int h = head0 + (lane & 15);
+            const float mt = fmaxf(fmaxf(red_s[h], red_s[64 + h]), fmaxf(red_s[128 + h], red_s[192 + h]));
+            const float ref = -lds_f(nref_s + 4 * h);
+            const bool move = mt > ref + kTcRefSlack;
+            const float f = ex2(ref - mt), fac = (move && ref != -INFINITY) ? f : 1.0f;
+            __syncwarp();
+            if (lane < 16) {
+              sts(fac_s + 4 * h, fac);
+              sts(nref_s + 4 * h, move ? -mt : -ref);
+            }
+          }
+          paged_bar(bar, 128);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[j] *= lds_f(fac_s + 4 * (head0 + j));
+          if (!first) {
+            // earlier tiles are in the accumulator, and their MMAs are done (s_full)
+#pragma unroll 1
+            for (int t = 0; t < 4; ++t) {
+              uint32_t r[16];
+              const uint32_t ta = tmem + lanes + 64 + 64 * t + head0;
+              tmem_ld_32x32b_x16(ta, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * lds_f(fac_s + 4 * (head0 + j)));
+              tmem_st_32x32b_x16(ta, r);
+              tmem_st_wait();
+            }
+          }
+          weights();
         }
-        // an FP8 window key's row scale goes into the weight that multiplies
-        // its codes; the sum takes the weights that the rounded products stand for
-        const float rs = win8 ? wsc_s[key] : 1.0f, inv = rs != 0.0f ? 1.0f / rs : 0.0f;
         uint32_t pk[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const __nv_bfloat162 v2 = __floats2bfloat162_rn(lj[2 * j] * rs, lj[2 * j + 1] * rs);
-          pk[j] = *reinterpret_cast<const uint32_t*>(&v2);
-          const float2 f = __bfloat1622float2(v2);
-          if (rs != 0.0f) { lj[2 * j] = f.x * inv; lj[2 * j + 1] = f.y * inv; }
+        for (int j = 0; j < 16; j += 2) {
+          sum[j] += y[j];                               // unrounded: the log-sum-exp keeps float32
+          sum[j + 1] += y[j + 1];
+          // an FP8 window key's row scale goes into the weight that multiplies its codes
+          pk[j / 2] = pack_bf16x2(y[j] * rs, y[j + 1] * rs);
         }
-        *reinterpret_cast<uint4*>(pt + sw128_off(key, 2 * hg)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(pt + sw128_off(key, 2 * hg + 1)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-        const float l = warp_reduce_heads16<false>(lj, lane);
-        if ((lane & 1) == 0) red_s[256 + quarter * 64 + 16 * hg + (lane >> 1)] = l;
+        sts(pt + sw128_off(key, 2 * hg), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        sts(pt + sw128_off(key, 2 * hg + 1), make_uint4(pk[4], pk[5], pk[6], pk[7]));
         fence_async_smem();
-        __syncthreads();
-        if (tid < 64) {
-          const int h = tid;
-          const float mt = fmaxf(fmaxf(red_s[h], red_s[64 + h]), fmaxf(red_s[128 + h], red_s[192 + h]));
-          const float ls = (red_s[256 + h] + red_s[320 + h]) + (red_s[384 + h] + red_s[448 + h]);
-          const float ref = ref_s[h];
-          const float nref = (mt > ref + kTcRefSlack) ? mt : ref;
-          const float f = (nref == ref || ref == -INFINITY) ? 1.0f : exp2f(ref - nref);
-          fac_s[h] = f;
-          if (f != 1.0f && !first) *rescale_flag = 1;
-          ref_s[h] = nref;
-          sum_s[h] = sum_s[h] * f + ls;
-        }
         tc_fence_before();
-        __syncthreads();
-      }
-      if (*rescale_flag) {
-        const int quarter = warp & 3, tt = warp >> 2;
-#pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t r[32];
-          const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 64 + 64 * tt + 32 * hh;
-          tc_fence_after();
-          tmem_ld_32x32b_x32(taddr, r);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * fac_s[32 * hh + j]);
-          tmem_st_32x32b_x32(taddr, r);
-          tmem_st_wait();
-        }
-        tc_fence_before();
-        __syncthreads();
-        if (tid == 0) *rescale_flag = 0;
-      }
-      // O^T += V^T . P^T
-      if (warp == 1 && lane == 0) {
-        tc_fence_after();
-        if (!*abort_flag) {
-          constexpr uint32_t idesc = umma_idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);
-          const uint32_t ka = smem_u32(kt), pa = smem_u32(pt);
-#pragma unroll
-          for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16(tmem + 64 + 64 * tt, umma_desc_sw128_mnmajor(ka + (2 * tt) * 16384 + kk * 2048, 16384),
-                        umma_desc_sw128_mnmajor(pa + kk * 2048, 16384), idesc, (!first || kk > 0) ? 1u : 0u);
-          }
-        }
-        umma_commit(&bars[2]);
-      }
-      // the key tile and P^T are free once MMA 2 is done
-      mbar_wait(&bars[2], ph_mma, kErrWaitTmemFull, abort_flag);
-      tc_fence_after();
-      ph_mma ^= 1;
-      __syncthreads();
-    }
-    ph_q ^= 1;
+        paged_arrive(p_full);
+        first = false;
 
-    // the query's result, or this CTA's partial of it
-    const bool whole = t0 == 0 && t1 == tiles;
-    const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
-    float* obuf = reinterpret_cast<float*>(kt);
-    if (!*abort_flag) {
-      const int quarter = warp & 3, tt = warp >> 2;
-      const int d = 128 * tt + 32 * quarter + lane;
+        if (c.t + 1 == c.t1) {
+          // -------------------------------------- the query's part is complete
+          const int row = c.row;
+          const bool whole = part_begins && c.t1 == c.tiles;
+          const int slot = 2 * blockIdx.x + (part_begins ? 1 : 0);
+          {
+            const float l = warp_reduce_heads16<false>(sum, lane);
+            if ((lane & 1) == 0) red_s[quarter * 64 + head0 + (lane >> 1)] = l;
+          }
+          paged_bar(bar, 128);
+          if (quarter == 0) {
+            const int h = head0 + (lane & 15);
+            const float l = (red_s[h] + red_s[64 + h]) + (red_s[128 + h] + red_s[192 + h]);
+            const float ref = -lds_f(nref_s + 4 * h), up = KVB ? 1.0f : kPagedFp4Up;
+            const float f = whole ? (l > 0.0f ? up / l : 0.0f) : up;
+            const float v = l > 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            __syncwarp();
+            if (lane < 16) {
+              sts(fac_s + 4 * h, f);
+              if (!*abort_flag) {
+                if (!whole) {
+                  *reinterpret_cast<float2*>(p.ml + (slot * 64 + h) * 2) = make_float2(ref, l);
+                } else if (p.lse) {
+                  p.lse[static_cast<int64_t>(row) * 64 + h] = v;
+                }
+              }
+            }
+          }
+          paged_bar(bar, 128);
+          paged_wait(o_full, ph_o, kErrWaitTmemFull, abort_flag);
+          tc_fence_after();
+          ph_o ^= 1;
+          const bool store = !*abort_flag;
+          // the channel of this lane's dim, and the lane with the next one (its partner)
+          const int ch = KVB ? lane : (lane & ~7) + paged_channel(lane & 7);
+          constexpr int kPair = KVB ? 1 : 2;
+          const int odd = ch & 1;
+          float fac[16];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 64 + 64 * tt + 32 * hh, r);
-        tmem_ld_wait();
+          for (int j = 0; j < 16; j += 4) {
+            const float4 f = lds_f4(fac_s + 4 * (head0 + j));
+            fac[j] = f.x; fac[j + 1] = f.y; fac[j + 2] = f.z; fac[j + 3] = f.w;
+          }
+#pragma unroll 1
+          for (int t = 0; t < 4; ++t) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(tmem + lanes + 64 + 64 * t + head0, r);
+            tmem_ld_wait();
+            const int d = 128 * t + 32 * quarter + ch;
+            if (whole) {
+              // lanes pair up: the even one writes dims d, d + 1 of head j, the odd one of head j + 1
+              __nv_bfloat16* op = p.out + (static_cast<int64_t>(row) * 64 + head0 + odd) * 512 + (d & ~1);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float l = sum_s[32 * hh + j];
-          obuf[(32 * hh + j) * 512 + d] = whole ? (l > 0.0f ? __uint_as_float(r[j]) / l : 0.0f) : __uint_as_float(r[j]);
+              for (int j = 0; j < 16; j += 2) {
+                const float a = __uint_as_float(r[j]) * fac[j], b = __uint_as_float(r[j + 1]) * fac[j + 1];
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, kPair);
+                const uint32_t v = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+                if (store) *reinterpret_cast<uint32_t*>(op + j * 512) = v;
+              }
+            } else if (store) {
+              float* op = p.opart + (static_cast<int64_t>(slot) * 64 + head0) * 512 + d;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) op[j * 512] = __uint_as_float(r[j]) * fac[j];
+            }
+          }
+          tc_fence_before();
+          paged_bar(bar, 128);                     // nref_s and fac_s are free
+          first = true;
         }
+        if (!paged_next(p, c)) break;
       }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (!*abort_flag) {
-      if (whole) {
-        uint4* op = reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(row) * 64 * 512);
-#pragma unroll 4
-        for (int j = tid; j < 64 * 512 / 8; j += kPagedThreads) {
-          const float4 a = reinterpret_cast<const float4*>(obuf)[2 * j];
-          const float4 c = reinterpret_cast<const float4*>(obuf)[2 * j + 1];
-          op[j] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(c.x, c.y), pack_bf16x2(c.z, c.w));
+      tc_fence_before();
+      paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));           // tensor memory is no longer read
+    } else {
+      PagedCursor c = paged_begin(p, range_s);
+      if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- MMA
+        // The whole warp walks along and one elected lane issues: the
+        // descriptors then live in uniform registers, and an MMA costs a few
+        // issue slots among busy warps.
+        const bool issuer = elect_one() && lane == 0;
+        uint32_t ph_q = 0;
+        int stage = 0;
+        bool first = true;
+        // descriptors of the tiles' first bytes; an offset adds to the 16-byte address field
+        const uint64_t kd = umma_desc_sw128_kmajor(kt), qd = umma_desc_sw128_kmajor(qt);
+        const uint64_t vd = umma_desc_sw128_mnmajor(kt, 16384), pd = umma_desc_sw128_mnmajor(pt, 16384);
+        constexpr uint32_t idesc1 = umma_idesc_bf16_f32(128, 64);
+        constexpr uint32_t idesc2 = umma_idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
+        for (uint32_t it = 0;; ++it) {
+          const uint32_t ph = it & 1;
+          const bool last = c.t + 1 == c.t1;
+          bool ok = true;
+          if (first) {
+            ok = paged_wait(q_full, ph_q, kErrWaitOperand, abort_flag);
+            ph_q ^= 1;
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            ok = paged_wait(&full[t], ph, kErrWaitTmaFull, abort_flag) && ok;
+            tc_fence_after();
+            if (ok && issuer) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16(tmem, kd + ((2 * t + (kk >> 2)) * 16384 + (kk & 3) * 32 >> 4),
+                          qd + ((2 * t + (kk >> 2)) * 8192 + (kk & 3) * 32 >> 4), idesc1, (t > 0 || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+          }
+          if (issuer) {
+            umma_commit(s_full);
+            if (last) umma_commit(q_free);
+          }
+          __syncwarp();
+          ok = paged_wait(p_full, ph, kErrWaitOperand, abort_flag) && ok;
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (ok && issuer) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16(tmem + 64 + 64 * t, vd + ((2 * t) * 16384 + kk * 2048 >> 4), pd + (kk * 2048 >> 4), idesc2,
+                          (!first || kk > 0) ? 1u : 0u);
+            }
+            if (issuer) umma_commit(&freed[t]);
+            __syncwarp();
+          }
+          first = last;
+          if (issuer) umma_commit(&rows_free[stage]);
+          if (last && issuer) umma_commit(o_full);
+          if (++stage == kPagedStages) stage = 0;
+          __syncwarp();
+          if (!paged_next(p, c)) break;
         }
-        if (p.lse && tid < 64) {
-          const float l = sum_s[tid];
-          p.lse[static_cast<int64_t>(row) * 64 + tid] = l > 0.0f ? (ref_s[tid] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
+        tc_fence_after();
+        tmem_dealloc(lds_i(misc32 + 160), 512);
+      } else if (warp == kMmaWarp + 1) {
+        // ---------------------------------------------------------- row addresses, 4 keys per lane
+        int stage = 0;
+        uint32_t ph = 1;
+        while (true) {
+          paged_wait(&rows_free[stage], ph, kErrWaitSmemEmpty, abort_flag);
+          const bool window = c.t >= c.kv_tiles;
+          const int b = c.row / p.Q;
+          const int key0 = (window ? c.t - c.kv_tiles : c.t) * kPagedKeys + lane;
+          const int bytes = window ? (p.swa_fp8 ? 512 : 1024) : (KVB ? 1024 : 288);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 32 * i;
+            const uint8_t* row = nullptr;
+            if (window) {
+              const int64_t r = static_cast<int64_t>(b) * p.swa_rows + static_cast<int64_t>(c.row - b * p.Q) * p.swa_step + key;
+              if (key < p.W) {
+                row = p.swa + r * bytes;
+                if (p.swa_fp8) sts(wsc_s + 4 * (stage * 128 + lane + 32 * i), p.swa_scale[r]);
+              }
+            } else if (key < c.keys) {
+              row = paged_row(p, p.table + b * p.ld_table, static_cast<uint32_t>(key), bytes);
+            }
+            sts(row_s + 8 * (stage * 128 + lane + 32 * i), row);
+            if (row)
+              for (int o = 0; o < bytes; o += 128) prefetch_l2(row + o);
+          }
+          if (lane == 0) sts(kind_s + 4 * stage, window ? (p.swa_fp8 ? kPagedFp8 : kPagedBf16) : kPagedPool);
+          paged_arrive(&rows_full[stage]);
+          if (!paged_next(p, c)) break;
+          if (++stage == kPagedStages) { stage = 0; ph ^= 1; }
         }
       } else {
-        float4* op = reinterpret_cast<float4*>(p.opart + static_cast<int64_t>(slot) * 64 * 512);
-        const float4* src = reinterpret_cast<const float4*>(obuf);
-#pragma unroll 4
-        for (int j = tid; j < 64 * 512 / 4; j += kPagedThreads) op[j] = src[j];
-        if (tid < 64) {
-          p.ml[(slot * 64 + tid) * 2] = ref_s[tid];
-          p.ml[(slot * 64 + tid) * 2 + 1] = sum_s[tid];
+        // ---------------------------------------------------------- Q
+        const int qtid = tid - 32 * (kMmaWarp + 2);
+        for (uint32_t part = 0;; ++part) {
+          paged_wait(q_free, (part & 1) ^ 1, kErrWaitOperand, abort_flag);
+          if (qtid == 0) {
+            uint64_t* arrived = KVB ? q_full : q_tma;
+            mbar_arrive_expect_tx(arrived, kTcQTileBytes);
+            const uint64_t pol = l2_policy_evict_first();
+            for (int k = 0; k < 8; ++k) tma_load_2d(smem + kTcKeyTileBytes + k * 8192, &tmap_q, arrived, 64 * k, c.row * 64, pol);
+          }
+          if (!KVB) {
+            paged_wait(q_tma, part & 1, kErrWaitOperand, abort_flag);
+            for (int i = qtid; i < static_cast<int>(kTcQTileBytes / 16); i += 4 * 32 * kPagedQWarps) {
+              uint4 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = i + k * 32 * kPagedQWarps;
+                if (j < static_cast<int>(kTcQTileBytes / 16)) v[k] = lds128(qt + 16 * j);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = i + k * 32 * kPagedQWarps;
+                if (j < static_cast<int>(kTcQTileBytes / 16)) sts(qt + 16 * j, paged_order(v[k]));
+              }
+            }
+            fence_async_smem();
+            paged_arrive(q_full);
+          }
+          c.left -= c.t1 - c.t;
+          if (c.left <= 0) break;
+          paged_enter(p, c, c.row + 1, 0);
         }
       }
     }
-    fence_async_smem();
-    __syncthreads();
-    at += t1 - t0;
-    offset = 0;
+  } else if (warp == kMmaWarp) {
+    tmem_dealloc(lds_i(misc32 + 160), 512);
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, 512); }
 }
 
-// Merge of the queries that range boundaries cut.  CTA column c looks at the
-// boundary before CTA c of the attention: when that CTA's range begins
-// inside a query and the one before it begins elsewhere, the query's
-// partials are CTA c-1's last and the first ones of CTAs c, c+1, ... as long
-// as they begin inside the same query.  One head per CTA, 4 dims per thread.
-__global__ void __launch_bounds__(128)
+// Merge of the queries that range boundaries cut.  A query that CTA c-1
+// begins and CTAs c, c+1, ... go on with left its partials in slots
+// 2(c-1)+1, 2c, 2(c+1), ...; CTA (h, y) here merges head h of the y-th such
+// query.  At most one query is cut per boundary, so there are at most
+// min(queries, CTAs - 1) of them.  Four thread groups take every fourth
+// partial each (128 threads x 4 dims, eight 16-byte loads in flight) and are
+// added in order: a fixed order whatever the timing.
+constexpr int kPagedJoinThreads = 512;
+__global__ void __launch_bounds__(kPagedJoinThreads)
 paged_attn_join_kernel(PagedAttnParams p, int ctas) {
+  __shared__ int c0_s, count_s[kPagedJoinThreads / 32];
+  __shared__ float w_s[kPagedMaxCtas + 1];              // factor of each partial
+  __shared__ int slot_s[kPagedMaxCtas + 1];             // and its slot
+  __shared__ float4 acc_s[3][128];
+  const int h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
+  if (tid == 0) c0_s = 0;
   pdl_wait();
-  const int h = blockIdx.x, c = blockIdx.y + 1, t = threadIdx.x;
-  const int row = p.first_row[c];
-  if (row < 0 || p.first_row[c - 1] == row) return;
-  int last = c;
-  while (last + 1 < ctas && p.first_row[last + 1] == row) ++last;
-  const int first_slot = 2 * (c - 1) + 1;
-  float M = p.ml[(first_slot * 64 + h) * 2];
-  for (int k = c; k <= last; ++k) M = fmaxf(M, p.ml[(2 * k * 64 + h) * 2]);
+  int begins = 0;
+  if (tid + 1 < ctas) {
+    const int r = __ldcg(p.first_row + tid + 1);
+    begins = r >= 0 && __ldcg(p.first_row + tid) != r;
+  }
+  const uint32_t vote = __ballot_sync(0xffffffffu, begins);
+  if (lane == 0) count_s[warp] = __popc(vote);
+  __syncthreads();
+  int rank = __popc(vote & ((1u << lane) - 1u));
+  for (int w = 0; w < warp; ++w) rank += count_s[w];
+  if (begins && rank == static_cast<int>(blockIdx.y)) c0_s = tid + 1;
+  __syncthreads();
+  const int c0 = c0_s;
+  if (c0 == 0) return;
+  const int row = __ldcg(p.first_row + c0);
+  const int n = 1 + __syncthreads_count(c0 + tid < ctas && __ldcg(p.first_row + c0 + tid) == row);   // partials
+  if (tid < n) slot_s[tid] = tid == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + tid - 1);
+  __syncthreads();
+  // every warp: joint maximum; thread i: the factor of partial i
+  const float2* ml = reinterpret_cast<const float2*>(p.ml) + h;
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(ml + slot_s[i] * 64).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if (tid < n) w_s[tid] = M == -INFINITY ? 0.0f : exp2f(__ldcg(ml + slot_s[tid] * 64).x - M);
+  __syncthreads();
   float L = 0.0f;
+  for (int i = lane; i < n; i += 32) L += w_s[i] * __ldcg(ml + slot_s[i] * 64).y;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+  const int g = tid >> 7, t = tid & 127;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != -INFINITY) {
-    for (int k = c - 1; k <= last; ++k) {
-      const int slot = k < c ? first_slot : 2 * k;
-      const float m = p.ml[(slot * 64 + h) * 2];
-      if (m == -INFINITY) continue;
-      const float f = exp2f(m - M);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(p.opart + (static_cast<int64_t>(slot) * 64 + h) * 512) + t);
-      L += f * p.ml[(slot * 64 + h) * 2 + 1];
-      acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
-    }
+  const float4* op = reinterpret_cast<const float4*>(p.opart + static_cast<int64_t>(h) * 512) + t;
+#pragma unroll 8
+  for (int i = g; i < n; i += 4) {
+    const float4 o = __ldcg(op + static_cast<int64_t>(slot_s[i]) * (64 * 512 / 4));
+    const float f = w_s[i];
+    acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
+  }
+  if (g > 0) acc_s[g - 1][t] = acc;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const float4 o = acc_s[k][t];
+    acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
   }
   const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
   uint2 packed;
