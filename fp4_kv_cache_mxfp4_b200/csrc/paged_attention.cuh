@@ -30,14 +30,15 @@
 // and P^T (16 KB) fill the shared memory, so the tile is filled in slabs of
 // 128 dims: MMA 2 releases slab t when its output rows t are done, and the
 // next tile's slab t is expanded while MMA 2 runs on the others.  Roles:
-//   warps 0-7    loaders: rows -> bf16 slabs (FP4 entries of the next tile
-//                wait in registers; bf16 rows go by cp.async)
-//   warps 8-23   softmax: S^T from tensor memory, weights to P^T, and the
-//                epilogue; warp w has keys 32 (w % 4).. and heads 16 (w / 4 - 2)..
-//   warp 24      MMA issue
-//   warp 25      row addresses of the tiles to come (block table, window),
+//   warp 0       MMA issue (the scheduler prefers older warps: as the last warp
+//                it lost hundreds of cycles per tile to the loaders)
+//   warp 1       row addresses of the tiles to come (block table, window),
 //                up to three tiles ahead, and their prefetch to L2
-//   warps 26-27  Q (TMA, then the channel order below)
+//   warps 2-3    Q (TMA, then the channel order below)
+//   warps 4-11   loaders: rows -> bf16 slabs (FP4 entries of the next tile
+//                wait in registers; bf16 rows go by cp.async)
+//   warps 12-27  softmax: S^T from tensor memory, weights to P^T, and the
+//                epilogue; warp w has keys 32 (w % 4).. and heads 16 (w / 4 - 3)..
 // Every role fits in the 72 registers that 28 warps leave each thread: with
 // the whole shared memory taken, L1 is too small for spilled values to stay,
 // and each reload then costs an L2 round trip (a version with some twenty
@@ -66,8 +67,14 @@
 namespace csa2 {
 
 constexpr int kPagedLoaders = 8, kPagedSoftmax = 16, kPagedQWarps = 2;      // warps
-constexpr int kPagedThreads = 32 * (kPagedLoaders + kPagedSoftmax + 2 + kPagedQWarps);
+constexpr int kPagedQWarp0 = 2, kPagedLoader0 = kPagedQWarp0 + kPagedQWarps, kPagedSoftmax0 = kPagedLoader0 + kPagedLoaders;
+constexpr int kPagedThreads = 32 * (kPagedSoftmax0 + kPagedSoftmax);
+static_assert(kPagedLoader0 % 4 == 0 && kPagedSoftmax0 % 4 == 0, "roles are whole warpgroups");
+// Registers per thread: 72 at launch (896 threads); warps 0-3 hand some to the loaders: 256 x 88 + 128 x 40 = 384 x 72.
+constexpr int kPagedLoaderRegs = 88, kPagedOtherRegs = 40;
+static_assert(256 * kPagedLoaderRegs + 128 * kPagedOtherRegs <= 384 * 72, "register split");
 constexpr int kPagedStages = 3;                        // tiles whose row addresses are kept
+constexpr uint32_t kPagedPolls = 1u << 24;            // of a wait, before it gives up
 constexpr int kPagedEndBar = 5;                         // named barriers: 1-4 the softmax quarters, 5 the end
 constexpr float kPagedFp4Up = 256.0f, kPagedFp4Down = 0.00390625f;
 constexpr int kPagedKeys = 128;                        // keys per tile (MMA M)
@@ -128,7 +135,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int6
 
 // Walks the tiles of a CTA's range: tiles [t, t1) of query `row`, then the next query's.
 struct PagedCursor {
-  int64_t left;              // tiles of the range from tile t on
+  uint32_t left;             // tiles of the range from tile t on (below 2^32 / 148 queries' worth each)
   int t, t1, tiles;          // this tile, the end of the range's part of the query, the query's tiles
   int row, keys, kv_tiles;
 };
@@ -137,18 +144,18 @@ __device__ __forceinline__ void paged_enter(const PagedAttnParams& p, PagedCurso
   c.tiles = paged_tiles(p, row, &c.keys);
   c.kv_tiles = (c.keys + kPagedKeys - 1) / kPagedKeys;
   c.t = offset;
-  c.t1 = static_cast<int>(min(static_cast<int64_t>(c.tiles), offset + c.left));
+  c.t1 = static_cast<int>(min(static_cast<int64_t>(c.tiles), static_cast<int64_t>(offset) + c.left));
 }
 // The cursor at the range's first tile.
 __device__ __forceinline__ PagedCursor paged_begin(const PagedAttnParams& p, const volatile PagedRange* r) {
   PagedCursor c;
-  c.left = r->hi - r->lo;
+  c.left = static_cast<uint32_t>(r->hi - r->lo);
   paged_enter(p, c, r->row, r->offset);
   return c;
 }
 // To the next tile; false behind the last.
 __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedCursor& c) {
-  if (--c.left <= 0) return false;
+  if (--c.left == 0) return false;
   if (++c.t == c.t1) paged_enter(p, c, c.row + 1, 0);
   return true;
 }
@@ -166,8 +173,18 @@ __device__ __forceinline__ const uint8_t* paged_row(const PagedAttnParams& p, co
 // others, the warp could go on in two parts, and what all lanes must execute
 // together (tcgen05, named barriers) then happened twice.
 __device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, int err, volatile int* abort) {
-  const bool ok = mbar_wait(bar, parity, err, abort);
-  return __all_sync(0xffffffffu, ok) != 0;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  // bounded by polls, which take some 140 cycles each: a second or two
+#pragma unroll 1
+  for (uint32_t n = 0; n < kPagedPolls && !*abort; ++n)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  __syncwarp();
+  if (!*abort) {
+    record_error(err);
+    *abort = 1;
+  }
+  __syncwarp();
+  return false;
 }
 __device__ __forceinline__ void paged_arrive(uint64_t* bar) {
   __syncwarp();
@@ -192,6 +209,10 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+template <int N>
+__device__ __forceinline__ void regs_up() { __syncwarp(); asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { __syncwarp(); asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 __device__ __forceinline__ void sts(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -228,6 +249,18 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// umma_bf16 with the descriptors' high words apart: only the low ones (the
+// addresses) change from one MMA to the next.
+__device__ __forceinline__ void paged_mma(uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+      :: "r"(tmem_d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
 }
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
@@ -282,11 +315,14 @@ __device__ __forceinline__ uint4 paged_expand8(uint32_t w, __nv_bfloat162 scale)
 
 constexpr int kPagedPool = 0, kPagedBf16 = 1, kPagedFp8 = 2;       // kinds of tiles: cache entries, window rows
 
-// Loader threads and keys.  FP4 entries: keys 16 w + 8 i + kk (i = 0, 1)
-// with kk from lane bits 1, 2 and 4 and the 16-byte unit of a 64-byte slab
-// piece from bits 0 and 3, so that 8 lanes of a store phase hit 8 different
-// bank groups of the swizzled tile and every global sector is used whole.
-// bf16 and FP8 rows: keys 16 w + 4 i + lane / 8 (i = 0..3), unit lane % 8.
+// Loader threads and keys (w counts the loader warps).  Warps 0-3 fill slabs
+// 0 and 2, warps 4-7 slabs 1 and 3: two slabs in work at a time, so that one's expansion covers the
+// other's stores and hand-over.  FP4 entries: keys 32 (w % 4) + 8 i + kk
+// (i = 0..3) with kk from lane bits 1, 2 and 4 and the 16-byte unit of a
+// 64-byte slab piece from bits 0 and 3, so that 8 lanes of a store phase hit
+// 8 different bank groups of the swizzled tile and every global sector is
+// used whole.  bf16 and FP8 rows: keys 32 (w % 4) + 4 i + lane / 8
+// (i = 0..7), unit lane % 8.
 
 template <bool KVB>
 __global__ void __launch_bounds__(kPagedThreads, 1)
@@ -301,7 +337,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t misc32 = pt + kTcPTileBytes;
   uint8_t* misc = smem + kTcKeyTileBytes + kTcQTileBytes + kTcPTileBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
-  uint64_t* full = bars;                                // [4] slab filled (8 loader warps)
+  uint64_t* full = bars;                                // [4] slab filled (4 loader warps)
   uint64_t* freed = bars + 4;                           // [4] slab read by MMA 2
   uint64_t* q_full = bars + 8;
   uint64_t* s_full = bars + 9;                          // MMA 1 done (and every MMA before it)
@@ -323,9 +359,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t wsc_s = misc32 + 5376;                               // float [3][128] FP8 row scales
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kMmaWarp = kPagedLoaders + kPagedSoftmax;
-  if (tid == 0) {
-    for (int i = 0; i < 4; ++i) { mbar_init(&full[i], kPagedLoaders); mbar_init(&freed[i], 1); }
+  if (tid == 32) {
+    for (int i = 0; i < 4; ++i) { mbar_init(&full[i], kPagedLoaders / 2); mbar_init(&freed[i], 1); }
     mbar_init(q_full, KVB ? 1 : kPagedQWarps);
     mbar_init(q_tma, 1);
     mbar_init(q_free, 1);
@@ -337,7 +372,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
-  if (warp == kMmaWarp) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+  if (warp == 0) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
   pdl_launch_dependents();
   pdl_wait();
   tc_fence_before();
@@ -352,26 +387,165 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   // the others return at once, and every role still walks to its end (the
   // named barriers stay matched), without writing results.
   if (range.lo < range.hi) {
-    if (warp < kPagedLoaders) {
+    if (warp < kPagedLoader0) {
+      regs_down<kPagedOtherRegs>();
+      PagedCursor c = paged_begin(p, range_s);
+      if (warp == 0) {
+        // ---------------------------------------------------------- MMA
+        // The whole warp walks along and one elected lane issues: the
+        // descriptors then live in uniform registers, and an MMA costs a few
+        // issue slots among busy warps.
+        const bool issuer = elect_one() && lane == 0;
+        uint32_t ph_q = 0;
+        int stage = 0;
+        bool first = true;
+        // descriptors of the tiles' first bytes; an offset adds to the 16-byte address field
+        const uint64_t kd = umma_desc_sw128_kmajor(kt), qd = umma_desc_sw128_kmajor(qt);
+        const uint64_t vd = umma_desc_sw128_mnmajor(kt, 16384), pd = umma_desc_sw128_mnmajor(pt, 16384);
+        constexpr uint32_t idesc1 = umma_idesc_bf16_f32(128, 64);
+        constexpr uint32_t idesc2 = umma_idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
+        for (uint32_t it = 0;; ++it) {
+          const uint32_t ph = it & 1;
+          const bool last = c.t + 1 == c.t1;
+          bool ok = true;
+          if (first) {
+            ok = paged_wait(q_full, ph_q, kErrWaitOperand, abort_flag);
+            ph_q ^= 1;
+          }
+          uint32_t da = static_cast<uint32_t>(kd), db = static_cast<uint32_t>(qd);
+#pragma unroll 1
+          for (int t = 0; t < 4; ++t) {
+            ok = paged_wait(&full[t], ph, kErrWaitTmaFull, abort_flag) && ok;
+            tc_fence_after();
+            if (ok && issuer) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                paged_mma(tmem, da + ((kk >> 2) * 16384 + (kk & 3) * 32 >> 4), kd >> 32,
+                          db + ((kk >> 2) * 8192 + (kk & 3) * 32 >> 4), qd >> 32, idesc1, (t > 0 || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+            da += 2 * 16384 >> 4;
+            db += 2 * 8192 >> 4;
+          }
+          if (issuer) {
+            umma_commit(s_full);
+            if (last) umma_commit(q_free);
+          }
+          __syncwarp();
+          ok = paged_wait(p_full, ph, kErrWaitOperand, abort_flag) && ok;
+          tc_fence_after();
+          da = static_cast<uint32_t>(vd);
+#pragma unroll 1
+          for (int t = 0; t < 4; ++t) {
+            if (ok && issuer) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                paged_mma(tmem + 64 + 64 * t, da + (kk * 2048 >> 4), vd >> 32, static_cast<uint32_t>(pd) + (kk * 2048 >> 4), pd >> 32,
+                          idesc2, (!first || kk > 0) ? 1u : 0u);
+            }
+            if (issuer) umma_commit(&freed[t]);
+            __syncwarp();
+            da += 2 * 16384 >> 4;
+          }
+          first = last;
+          if (issuer) umma_commit(&rows_free[stage]);
+          if (last && issuer) umma_commit(o_full);
+          if (++stage == kPagedStages) stage = 0;
+          __syncwarp();
+          if (!paged_next(p, c)) break;
+        }
+        paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
+        tc_fence_after();
+        tmem_dealloc(lds_i(misc32 + 160), 512);
+      } else if (warp == 1) {
+        // ---------------------------------------------------------- row addresses, 4 keys per lane
+        int stage = 0;
+        uint32_t ph = 1;
+        while (true) {
+          paged_wait(&rows_free[stage], ph, kErrWaitSmemEmpty, abort_flag);
+          const bool window = c.t >= c.kv_tiles;
+          const int b = c.row / p.Q;
+          const int key0 = (window ? c.t - c.kv_tiles : c.t) * kPagedKeys + lane;
+          const int bytes = window ? (p.swa_fp8 ? 512 : 1024) : (KVB ? 1024 : 288);
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 32 * i;
+            const uint8_t* row = nullptr;
+            if (window) {
+              const int64_t r = static_cast<int64_t>(b) * p.swa_rows + static_cast<int64_t>(c.row - b * p.Q) * p.swa_step + key;
+              if (key < p.W) {
+                row = p.swa + r * bytes;
+                if (p.swa_fp8) sts(wsc_s + 4 * (stage * 128 + lane + 32 * i), p.swa_scale[r]);
+              }
+            } else if (key < c.keys) {
+              row = paged_row(p, p.table + b * p.ld_table, static_cast<uint32_t>(key), bytes);
+            }
+            sts(row_s + 8 * (stage * 128 + lane + 32 * i), row);
+            if (row)
+              for (int o = 0; o < bytes; o += 128) prefetch_l2(row + o);
+          }
+          if (lane == 0) sts(kind_s + 4 * stage, window ? (p.swa_fp8 ? kPagedFp8 : kPagedBf16) : kPagedPool);
+          paged_arrive(&rows_full[stage]);
+          if (!paged_next(p, c)) break;
+          if (++stage == kPagedStages) { stage = 0; ph ^= 1; }
+        }
+      } else {
+        // ---------------------------------------------------------- Q
+        const int qtid = tid - 32 * kPagedQWarp0;
+        for (uint32_t part = 0;; ++part) {
+          paged_wait(q_free, (part & 1) ^ 1, kErrWaitOperand, abort_flag);
+          if (qtid == 0) {
+            uint64_t* arrived = KVB ? q_full : q_tma;
+            mbar_arrive_expect_tx(arrived, kTcQTileBytes);
+            const uint64_t pol = l2_policy_evict_first();
+            for (int k = 0; k < 8; ++k) tma_load_2d(smem + kTcKeyTileBytes + k * 8192, &tmap_q, arrived, 64 * k, c.row * 64, pol);
+          }
+          if (!KVB) {
+            paged_wait(q_tma, part & 1, kErrWaitOperand, abort_flag);
+            for (int i = qtid; i < static_cast<int>(kTcQTileBytes / 16); i += 4 * 32 * kPagedQWarps) {
+              uint4 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = i + k * 32 * kPagedQWarps;
+                if (j < static_cast<int>(kTcQTileBytes / 16)) v[k] = lds128(qt + 16 * j);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int j = i + k * 32 * kPagedQWarps;
+                if (j < static_cast<int>(kTcQTileBytes / 16)) sts(qt + 16 * j, paged_order(v[k]));
+              }
+            }
+            fence_async_smem();
+            paged_arrive(q_full);
+          }
+          c.left -= c.t1 - c.t;
+          if (c.left == 0) break;
+          paged_enter(p, c, c.row + 1, 0);
+        }
+      }
+    } else if (warp < kPagedSoftmax0) {
       // ------------------------------------------------------------ loaders
-      int64_t left = range_s->hi - range_s->lo;
+      regs_up<kPagedLoaderRegs>();
+      uint32_t left = static_cast<uint32_t>(range_s->hi - range_s->lo);
       const int kk = ((lane >> 1) & 3) | ((lane >> 2) & 4), u = (lane & 1) | ((lane >> 2) & 2);
-      uint4 raw[4][2];                                  // FP4: [slab][key] 32 channels ...
-      uint16_t rsc[4][2];                               // ... and their two scales
+      const int key0 = 32 * (warp & 3), t0 = (warp - kPagedLoader0) >> 2;  // first key; slabs t0, t0 + 2
+      uint4 raw[2][4];                                  // FP4: [slab][key] 32 channels ...
+      uint16_t rsc[2][4];                               // ... and their two scales
       int kind;
       auto fetch = [&](int stage) {                     // the tile's kind and, of cache entries, their bytes
         kind = lds_i(kind_s + 4 * stage);
         if (!KVB && kind == kPagedPool) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t* row = lds_ptr(row_s + 8 * (stage * 128 + 16 * warp + 8 * i + kk));
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* row = lds_ptr(row_s + 8 * (stage * 128 + key0 + 8 * i + kk));
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              raw[t][i] = make_uint4(0, 0, 0, 0);
-              rsc[t][i] = 0;
+            for (int k = 0; k < 2; ++k) {
+              const int t = t0 + 2 * k;
+              raw[k][i] = make_uint4(0, 0, 0, 0);
+              rsc[k][i] = 0;
               if (row) {
-                raw[t][i] = __ldg(reinterpret_cast<const uint4*>(row + 64 * t + 16 * u));
-                rsc[t][i] = __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 8 * t + 2 * u));
+                raw[k][i] = __ldg(reinterpret_cast<const uint4*>(row + 64 * t + 16 * u));
+                rsc[k][i] = __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 8 * t + 2 * u));
               }
             }
           }
@@ -387,62 +561,63 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
       uint32_t ph_rows = 0;
       for (uint32_t ph = 1;; ph ^= 1) {                 // ph: MMA 2 of the tile before has released the slab
         if (!KVB && kind == kPagedPool) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t chunk = kt + (2 * t + (u >> 1)) * 16384;
-            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const __nv_bfloat162 sc = paged_scales(rsc[t][i]);
-              const __nv_bfloat162 s0 = __low2bfloat162(sc), s1 = __high2bfloat162(sc);
-              const uint32_t w[4] = {raw[t][i].x, raw[t][i].y, raw[t][i].z, raw[t][i].w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                sts(chunk + sw128_off(16 * warp + 8 * i + kk, 4 * (u & 1) + q), paged_expand8(w[q], q < 2 ? s0 : s1));
-            }
-            publish(t);
-          }
-        } else if (KVB && kind == kPagedPool) {
-          const uint8_t* row[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) row[i] = lds_ptr(row_s + 8 * (stage * 128 + 16 * warp + 4 * i + (lane >> 3)));
-          auto copy = [&](int t) {
+          // (rolled: the kernel's hot code should stay in the instruction cache)
+          uint32_t chunk = kt + (2 * t0 + (u >> 1)) * 16384 + sw128_off(key0 + kk, 4 * (u & 1));
+#pragma unroll 1
+          for (int t = t0; t < 4; t += 2) {
             paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 sc = paged_scales(rsc[0][i]);
+              const __nv_bfloat162 s0 = __low2bfloat162(sc), s1 = __high2bfloat162(sc);
+              const uint32_t w[4] = {raw[0][i].x, raw[0][i].y, raw[0][i].z, raw[0][i].w};
+              // unit q of the row: the swizzle XORs bits 4, 5 of the address
+#pragma unroll
+              for (int q = 0; q < 4; ++q) sts((chunk ^ (16 * q)) + 1024 * i, paged_expand8(w[q], q < 2 ? s0 : s1));
+            }
+            publish(t);
+            chunk += 4 * 16384;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              raw[0][i] = raw[1][i];
+              rsc[0][i] = rsc[1][i];
+            }
+          }
+        } else if (KVB && kind == kPagedPool) {
+          const uint8_t* row[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) row[i] = lds_ptr(row_s + 8 * (stage * 128 + key0 + 4 * i + (lane >> 3)));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = t0 + 2 * k;
+            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
               const uint8_t* src = row[i] ? row[i] + 256 * t + 16 * (lane & 7) : p.kv;
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                cp_async16(kt + (2 * t + h) * 16384 + sw128_off(16 * warp + 4 * i + (lane >> 3), lane & 7),
+                cp_async16(kt + (2 * t + h) * 16384 + sw128_off(key0 + 4 * i + (lane >> 3), lane & 7),
                            src + (row[i] ? 128 * h : 0), row[i] != nullptr);
             }
             cp_async_commit();
-          };
-          copy(0);
-          copy(1);
-          copy(2);
-          cp_async_wait<2>();
-          publish(0);
-          copy(3);
-          cp_async_wait<2>();
-          publish(1);
+          }
           cp_async_wait<1>();
-          publish(2);
+          publish(t0);
           cp_async_wait<0>();
-          publish(3);
+          publish(t0 + 2);
         } else {
-          // window rows, in the pool's channel order, half a slab's rows at a time
+          // window rows, in the pool's channel order, two keys of a thread at a time
           const bool fp8 = kind == kPagedFp8;
 #pragma unroll 1
-          for (int t = 0; t < 4; ++t) {
+          for (int t = t0; t < 4; t += 2) {
             paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
+            for (int i = 0; i < 8; i += 2) {
               const uint8_t* row[2];
               uint4 x[2][2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                row[k] = lds_ptr(row_s + 8 * (stage * 128 + 16 * warp + 4 * (i + k) + (lane >> 3)));
+                row[k] = lds_ptr(row_s + 8 * (stage * 128 + key0 + 4 * (i + k) + (lane >> 3)));
                 x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
                 if (row[k]) {
                   const uint4* src = reinterpret_cast<const uint4*>(row[k] + (fp8 ? 128 : 256) * t) + (lane & 7);
@@ -452,7 +627,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               }
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int r = 16 * warp + 4 * (i + k) + (lane >> 3);
+                const int r = key0 + 4 * (i + k) + (lane >> 3);
                 uint4 lo = x[k][0], hi = x[k][1];
                 uint32_t at = 2 * t * 16384 + sw128_off(r, lane & 7), at2 = at + 16384;
                 if (fp8) {
@@ -471,15 +646,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             publish(t);
           }
         }
-        if (--left <= 0) break;
+        if (--left == 0) break;
         if (++stage == kPagedStages) { stage = 0; ph_rows ^= 1; }
         paged_wait(&rows_full[stage], ph_rows, kErrWaitOperand, abort_flag);
         fetch(stage);                                   // behind the tile's last fence, which would wait for the loads
       }
-    } else if (warp < kMmaWarp) {
+    } else {
       // ------------------------------------------------------------ softmax
       PagedCursor c = paged_begin(p, range_s);
-      const int quarter = warp & 3, hg = (warp - kPagedLoaders) >> 2, bar = 1 + hg;
+      const int quarter = warp & 3, hg = (warp - kPagedSoftmax0) >> 2, bar = 1 + hg;
       const int key = 32 * quarter + lane, head0 = 16 * hg;
       const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
       uint32_t ph_o = 0;
@@ -495,7 +670,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           paged_bar(bar, 128);
         }
         const bool window = c.t >= c.kv_tiles;
-        paged_wait(&full[0], it & 1, kErrWaitSmemEmpty, abort_flag);      // the loaders have seen the tile's addresses
+        paged_wait(&full[0], it & 1, kErrWaitSmemEmpty, abort_flag);      // a loader has seen the tile's addresses
         const bool there = lds_ptr(row_s + 8 * (stage * 128 + key)) != nullptr;
         float rs = (window && p.swa_fp8) ? lds_f(wsc_s + 4 * (stage * 128 + key)) : 1.0f;
         if (++stage == kPagedStages) stage = 0;
@@ -503,7 +678,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         if (!KVB && window) rs *= kPagedFp4Down;
         paged_wait(s_full, it & 1, kErrWaitTmemFull, abort_flag);
         tc_fence_after();
-        // y = exp2(logit - reference) in log2 units; a head without a reference yet has +inf
+        // y = exp2(logit - reference) in log2 units; a head without a reference
+        // yet has +inf.  The weights go to P^T before the vote on whether some
+        // reference must move (then they are made again), and into the sums
+        // after the hand-over: both off the path from S^T to MMA 2.
         float y[16];
         float over = -INFINITY;
         auto weights = [&]() {
@@ -518,13 +696,25 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             y[j + 2] = fmaf(__uint_as_float(r[j + 2]), ls, nr.z);
             y[j + 3] = fmaf(__uint_as_float(r[j + 3]), ls, nr.w);
           }
+          if (!__all_sync(0xffffffffu, there)) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = there ? y[j] : -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            over = fmaxf(over, y[j]);
-            y[j] = ex2(y[j]);
+            for (int j = 0; j < 16; ++j) y[j] = there ? y[j] : -INFINITY;
           }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              const int i = 8 * q + j;
+              over = fmaxf(over, fmaxf(y[i], y[i + 1]));
+              y[i] = ex2(y[i]);
+              y[i + 1] = ex2(y[i + 1]);
+              // an FP8 window key's row scale goes into the weight that multiplies its codes
+              pk[j / 2] = window ? pack_bf16x2(y[i] * rs, y[i + 1] * rs) : pack_bf16x2(y[i], y[i + 1]);
+            }
+            sts(pt + sw128_off(key, 2 * hg + q), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          }
+          fence_async_smem();
         };
         weights();
         if (named_bar_or(bar, 128, over > kTcRefSlack)) {
@@ -571,19 +761,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           }
           weights();
         }
-        uint32_t pk[8];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          sum[j] += y[j];                               // unrounded: the log-sum-exp keeps float32
-          sum[j + 1] += y[j + 1];
-          // an FP8 window key's row scale goes into the weight that multiplies its codes
-          pk[j / 2] = pack_bf16x2(y[j] * rs, y[j + 1] * rs);
-        }
-        sts(pt + sw128_off(key, 2 * hg), make_uint4(pk[0], pk[1], pk[2], pk[3]));
-        sts(pt + sw128_off(key, 2 * hg + 1), make_uint4(pk[4], pk[5], pk[6], pk[7]));
-        fence_async_smem();
         tc_fence_before();
         paged_arrive(p_full);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[j] += y[j];    // unrounded: the log-sum-exp keeps float32
         first = false;
 
         if (c.t + 1 == c.t1) {
@@ -659,138 +840,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
       }
       tc_fence_before();
       paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));           // tensor memory is no longer read
-    } else {
-      PagedCursor c = paged_begin(p, range_s);
-      if (warp == kMmaWarp) {
-        // ---------------------------------------------------------- MMA
-        // The whole warp walks along and one elected lane issues: the
-        // descriptors then live in uniform registers, and an MMA costs a few
-        // issue slots among busy warps.
-        const bool issuer = elect_one() && lane == 0;
-        uint32_t ph_q = 0;
-        int stage = 0;
-        bool first = true;
-        // descriptors of the tiles' first bytes; an offset adds to the 16-byte address field
-        const uint64_t kd = umma_desc_sw128_kmajor(kt), qd = umma_desc_sw128_kmajor(qt);
-        const uint64_t vd = umma_desc_sw128_mnmajor(kt, 16384), pd = umma_desc_sw128_mnmajor(pt, 16384);
-        constexpr uint32_t idesc1 = umma_idesc_bf16_f32(128, 64);
-        constexpr uint32_t idesc2 = umma_idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
-        for (uint32_t it = 0;; ++it) {
-          const uint32_t ph = it & 1;
-          const bool last = c.t + 1 == c.t1;
-          bool ok = true;
-          if (first) {
-            ok = paged_wait(q_full, ph_q, kErrWaitOperand, abort_flag);
-            ph_q ^= 1;
-          }
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            ok = paged_wait(&full[t], ph, kErrWaitTmaFull, abort_flag) && ok;
-            tc_fence_after();
-            if (ok && issuer) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16(tmem, kd + ((2 * t + (kk >> 2)) * 16384 + (kk & 3) * 32 >> 4),
-                          qd + ((2 * t + (kk >> 2)) * 8192 + (kk & 3) * 32 >> 4), idesc1, (t > 0 || kk > 0) ? 1u : 0u);
-            }
-            __syncwarp();
-          }
-          if (issuer) {
-            umma_commit(s_full);
-            if (last) umma_commit(q_free);
-          }
-          __syncwarp();
-          ok = paged_wait(p_full, ph, kErrWaitOperand, abort_flag) && ok;
-          tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if (ok && issuer) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16(tmem + 64 + 64 * t, vd + ((2 * t) * 16384 + kk * 2048 >> 4), pd + (kk * 2048 >> 4), idesc2,
-                          (!first || kk > 0) ? 1u : 0u);
-            }
-            if (issuer) umma_commit(&freed[t]);
-            __syncwarp();
-          }
-          first = last;
-          if (issuer) umma_commit(&rows_free[stage]);
-          if (last && issuer) umma_commit(o_full);
-          if (++stage == kPagedStages) stage = 0;
-          __syncwarp();
-          if (!paged_next(p, c)) break;
-        }
-        paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
-        tc_fence_after();
-        tmem_dealloc(lds_i(misc32 + 160), 512);
-      } else if (warp == kMmaWarp + 1) {
-        // ---------------------------------------------------------- row addresses, 4 keys per lane
-        int stage = 0;
-        uint32_t ph = 1;
-        while (true) {
-          paged_wait(&rows_free[stage], ph, kErrWaitSmemEmpty, abort_flag);
-          const bool window = c.t >= c.kv_tiles;
-          const int b = c.row / p.Q;
-          const int key0 = (window ? c.t - c.kv_tiles : c.t) * kPagedKeys + lane;
-          const int bytes = window ? (p.swa_fp8 ? 512 : 1024) : (KVB ? 1024 : 288);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 32 * i;
-            const uint8_t* row = nullptr;
-            if (window) {
-              const int64_t r = static_cast<int64_t>(b) * p.swa_rows + static_cast<int64_t>(c.row - b * p.Q) * p.swa_step + key;
-              if (key < p.W) {
-                row = p.swa + r * bytes;
-                if (p.swa_fp8) sts(wsc_s + 4 * (stage * 128 + lane + 32 * i), p.swa_scale[r]);
-              }
-            } else if (key < c.keys) {
-              row = paged_row(p, p.table + b * p.ld_table, static_cast<uint32_t>(key), bytes);
-            }
-            sts(row_s + 8 * (stage * 128 + lane + 32 * i), row);
-            if (row)
-              for (int o = 0; o < bytes; o += 128) prefetch_l2(row + o);
-          }
-          if (lane == 0) sts(kind_s + 4 * stage, window ? (p.swa_fp8 ? kPagedFp8 : kPagedBf16) : kPagedPool);
-          paged_arrive(&rows_full[stage]);
-          if (!paged_next(p, c)) break;
-          if (++stage == kPagedStages) { stage = 0; ph ^= 1; }
-        }
-      } else {
-        // ---------------------------------------------------------- Q
-        const int qtid = tid - 32 * (kMmaWarp + 2);
-        for (uint32_t part = 0;; ++part) {
-          paged_wait(q_free, (part & 1) ^ 1, kErrWaitOperand, abort_flag);
-          if (qtid == 0) {
-            uint64_t* arrived = KVB ? q_full : q_tma;
-            mbar_arrive_expect_tx(arrived, kTcQTileBytes);
-            const uint64_t pol = l2_policy_evict_first();
-            for (int k = 0; k < 8; ++k) tma_load_2d(smem + kTcKeyTileBytes + k * 8192, &tmap_q, arrived, 64 * k, c.row * 64, pol);
-          }
-          if (!KVB) {
-            paged_wait(q_tma, part & 1, kErrWaitOperand, abort_flag);
-            for (int i = qtid; i < static_cast<int>(kTcQTileBytes / 16); i += 4 * 32 * kPagedQWarps) {
-              uint4 v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int j = i + k * 32 * kPagedQWarps;
-                if (j < static_cast<int>(kTcQTileBytes / 16)) v[k] = lds128(qt + 16 * j);
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int j = i + k * 32 * kPagedQWarps;
-                if (j < static_cast<int>(kTcQTileBytes / 16)) sts(qt + 16 * j, paged_order(v[k]));
-              }
-            }
-            fence_async_smem();
-            paged_arrive(q_full);
-          }
-          c.left -= c.t1 - c.t;
-          if (c.left <= 0) break;
-          paged_enter(p, c, c.row + 1, 0);
-        }
-      }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == 0) {
     tmem_dealloc(lds_i(misc32 + 160), 512);
   }
 }
