@@ -169,7 +169,8 @@ csa2_status device_info(DeviceInfo** out) {
         set_smem_attrs(paged_rows_kernel, 0) != cudaSuccess ||
         set_smem_attrs(paged_attn_kernel<false>, static_cast<int>(kPagedSmem)) != cudaSuccess ||
         set_smem_attrs(paged_attn_kernel<true>, static_cast<int>(kPagedSmem)) != cudaSuccess ||
-        set_smem_attrs(paged_attn_join_kernel, 0) != cudaSuccess)
+        set_smem_attrs(paged_attn_join_kernel<true>, 0) != cudaSuccess ||
+        set_smem_attrs(paged_attn_join_kernel<false>, 0) != cudaSuccess)
       return CSA2_ERR_CUDA;
     d.topk_max_cluster = topk_cluster_limit();
     if (!g_encode) {
@@ -663,14 +664,14 @@ int paged_ctas(const csa2_paged_attn_args* a) {
   return static_cast<int>(std::min<int64_t>(kPagedMaxCtas, tiles * a->B * a->Q));
 }
 
-struct PagedWs { size_t opart, ml, first, total; };
+struct PagedWs { size_t opart, ml, cut, total; };
 PagedWs paged_ws(const csa2_paged_attn_args* a) {
   const size_t n = paged_ctas(a);
   PagedWs w;
   w.opart = 0;
   w.ml = w.opart + 2 * n * 64 * 512 * 4;
-  w.first = w.ml + 2 * n * 64 * 2 * 4;
-  w.total = up256(w.first + n * 4);
+  w.cut = w.ml + 2 * n * 64 * 2 * 4;
+  w.total = up256(w.cut + n * 8);
   return w;
 }
 
@@ -694,7 +695,7 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   p.lse = a->lse;
   p.opart = reinterpret_cast<float*>(wb + w.opart);
   p.ml = reinterpret_cast<float*>(wb + w.ml);
-  p.first_row = reinterpret_cast<int32_t*>(wb + w.first);
+  p.cut = reinterpret_cast<int2*>(wb + w.cut);
   CUtensorMap tq;
   if (!make_map_bf16_512(&tq, a->q, static_cast<uint64_t>(p.BQ) * 64, 64)) return CSA2_ERR_CUDA;
   const int ctas = std::min(paged_ctas(a), dev.sms);
@@ -705,7 +706,10 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   if (e != cudaSuccess) return CSA2_ERR_CUDA;
   if (ctas == 1) return CSA2_OK;                       // no range boundary
   trace_pre(kKPagedJoin, st);
-  e = launch_ex(paged_attn_join_kernel, dim3(64, static_cast<unsigned>(std::min(p.BQ, ctas - 1))),
+  // a cut query has (CTAs + queries) / queries partials or so
+  const bool split = p.BQ <= kPagedSplitJoin;
+  e = launch_ex(split ? paged_attn_join_kernel<true> : paged_attn_join_kernel<false>,
+                split ? dim3(64, static_cast<unsigned>(std::min(p.BQ, ctas - 1))) : dim3(16, static_cast<unsigned>(ctas - 1)),
                 dim3(kPagedJoinThreads), 0, st, 0, p, ctas);
   trace_post(st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;

@@ -97,7 +97,7 @@ struct PagedAttnParams {
   float* lse;                // optional [BQ][64]
   float* opart;              // [2 * CTAs][64][512] unnormalised partials
   float* ml;                 // [2 * CTAs][64][2]: reference (log2 units), sum
-  int32_t* first_row;        // [CTAs]: the query a CTA's range begins inside of, -1 if it begins with a new one
+  int2* cut;                 // [CTAs]: (query, partials) where a CTA's range is the first to begin inside a query, else (-1, 0)
 };
 
 // Tiles of query r: at least one, so that a query without any key is written too.
@@ -110,7 +110,7 @@ __device__ __forceinline__ int paged_tiles(const PagedAttnParams& p, int r, int*
 // This CTA's tile range [lo, hi) of the total, the query that lo lies in and
 // lo's offset inside it.  Every CTA sums the tiles of all queries (4 bytes
 // each from L2); every thread calls it.
-struct PagedRange { int64_t lo, hi; int row, offset; };
+struct PagedRange { int64_t lo, hi; int row, offset, parts; };   // parts: partials of the query, as in cut[]
 __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int64_t* warp_s, PagedRange* range_s) {
   const int per = (p.BQ + blockDim.x - 1) / blockDim.x;
   const int r0 = min(p.BQ, static_cast<int>(threadIdx.x) * per), r1 = min(p.BQ, r0 + per);
@@ -120,12 +120,19 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int6
   int64_t at = block_exclusive_sum(mine, warp_s, &total);
   // no CTA without a tile between two that have one (the join looks at neighbours)
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-  if (blockIdx.x >= ctas) return PagedRange{0, 0, 0, 0};
+  if (blockIdx.x >= ctas) return PagedRange{0, 0, 0, 0, 0};
   const int64_t lo = total * blockIdx.x / ctas, hi = total * (blockIdx.x + 1) / ctas;
   if (lo >= at && lo < at + mine) {
     for (int r = r0; r < r1; ++r) {
       const int t = paged_tiles(p, r, &keys);
-      if (lo < at + t) { *range_s = PagedRange{lo, hi, r, static_cast<int>(lo - at)}; break; }
+      if (lo < at + t) {
+        // tile x lies in the range of CTA ((x + 1) ctas - 1) / total
+        const int first = static_cast<int>(((at + 1) * ctas - 1) / total);
+        const int last = static_cast<int>(((at + t) * ctas - 1) / total);
+        const bool cuts = lo > at && static_cast<int>(blockIdx.x) == first + 1;
+        *range_s = PagedRange{lo, hi, r, static_cast<int>(lo - at), cuts ? last - first + 1 : 0};
+        break;
+      }
       at += t;
     }
   }
@@ -381,7 +388,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   // (read by asm: only asm writes it, which a plain load might not be told)
   const uint32_t tmem = lds_i(misc32 + 160);
   const PagedRange range = paged_range(p, warp_s, range_s);
-  if (tid == 0) p.first_row[blockIdx.x] = (range.lo < range.hi && range.offset > 0) ? range.row : -1;
+  if (tid == 0) p.cut[blockIdx.x] = range.parts > 0 ? make_int2(range.row, range.parts) : make_int2(-1, 0);
 
   // Every role walks the same tiles.  Waits are bounded; after one gave up
   // the others return at once, and every role still walks to its end (the
@@ -404,9 +411,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         const uint64_t vd = umma_desc_sw128_mnmajor(kt, 16384), pd = umma_desc_sw128_mnmajor(pt, 16384);
         constexpr uint32_t idesc1 = umma_idesc_bf16_f32(128, 64);
         constexpr uint32_t idesc2 = umma_idesc_bf16_f32(128, 64) | (1u << 15) | (1u << 16);   // both MN-major
-        for (uint32_t it = 0;; ++it) {
-          const uint32_t ph = it & 1;
-          const bool last = c.t + 1 == c.t1;
+        // The walk to the next tile is done while the softmax runs: between MMA 2
+        // and the next MMA 1 every instruction costs (28 warps share the
+        // instruction cache).
+        bool last = c.t + 1 == c.t1;
+        for (uint32_t ph = 0;; ph ^= 1) {
           bool ok = true;
           if (first) {
             ok = paged_wait(q_full, ph_q, kErrWaitOperand, abort_flag);
@@ -432,6 +441,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             if (last) umma_commit(q_free);
           }
           __syncwarp();
+          const bool more = paged_next(p, c), next_last = c.t + 1 == c.t1;
           ok = paged_wait(p_full, ph, kErrWaitOperand, abort_flag) && ok;
           tc_fence_after();
           da = static_cast<uint32_t>(vd);
@@ -447,12 +457,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             __syncwarp();
             da += 2 * 16384 >> 4;
           }
-          first = last;
-          if (issuer) umma_commit(&rows_free[stage]);
-          if (last && issuer) umma_commit(o_full);
-          if (++stage == kPagedStages) stage = 0;
+          if (issuer) {
+            umma_commit(&rows_free[stage]);
+            if (last) umma_commit(o_full);
+          }
           __syncwarp();
-          if (!paged_next(p, c)) break;
+          if (!more) break;
+          first = last;
+          last = next_last;
+          if (++stage == kPagedStages) stage = 0;
         }
         paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
         tc_fence_after();
@@ -848,68 +861,89 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 
 // Merge of the queries that range boundaries cut.  A query that CTA c-1
 // begins and CTAs c, c+1, ... go on with left its partials in slots
-// 2(c-1)+1, 2c, 2(c+1), ...; CTA (h, y) here merges head h of the y-th such
-// query.  At most one query is cut per boundary, so there are at most
-// min(queries, CTAs - 1) of them.  Four thread groups take every fourth
-// partial each (128 threads x 4 dims, eight 16-byte loads in flight) and are
-// added in order: a fixed order whatever the timing.
+// 2(c-1)+1, 2c, 2(c+1), ...; cut[c] names it and counts them.  Partials are
+// added in a fixed order whatever the timing.
+//
+// SPLIT (few queries, many partials each): CTA (h, y) takes head h of the
+// y-th cut query, its four thread groups every fourth partial each.  Else
+// (many queries, few partials each): CTA (x, y) takes boundary y + 1, if a
+// query is first cut there, and its four groups one head each.
+// 128 threads x 4 dims per group, four 16-byte loads in flight.
 constexpr int kPagedJoinThreads = 512;
+constexpr int kPagedSplitJoin = 16;                    // up to this many queries SPLIT
+template <bool SPLIT>
 __global__ void __launch_bounds__(kPagedJoinThreads)
 paged_attn_join_kernel(PagedAttnParams p, int ctas) {
   __shared__ int c0_s, count_s[kPagedJoinThreads / 32];
-  __shared__ float w_s[kPagedMaxCtas + 1];              // factor of each partial
-  __shared__ int slot_s[kPagedMaxCtas + 1];             // and its slot
+  __shared__ int slot_s[kPagedMaxCtas + 1];              // slot of each partial
+  __shared__ float w_s[4][kPagedMaxCtas + 1];            // and its factor, per head of the CTA
   __shared__ float4 acc_s[3][128];
-  const int h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = tid >> 7, t = tid & 127;
+  const int h = SPLIT ? blockIdx.x : 4 * blockIdx.x + g;
   pdl_launch_dependents();
-  if (tid == 0) c0_s = 0;
+  if (SPLIT && tid == 0) c0_s = 0;
   pdl_wait();
-  int begins = 0;
-  if (tid + 1 < ctas) {
-    const int r = __ldcg(p.first_row + tid + 1);
-    begins = r >= 0 && __ldcg(p.first_row + tid) != r;
+  int c0 = blockIdx.y + 1;
+  if (SPLIT) {
+    const bool begins = tid + 1 < ctas && __ldcg(&p.cut[tid + 1].y) > 0;
+    const uint32_t vote = __ballot_sync(0xffffffffu, begins);
+    if (lane == 0) count_s[warp] = __popc(vote);
+    __syncthreads();
+    int rank = __popc(vote & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) rank += count_s[w];
+    if (begins && rank == static_cast<int>(blockIdx.y)) c0_s = tid + 1;
+    __syncthreads();
+    c0 = c0_s;
+    if (c0 == 0) return;
   }
-  const uint32_t vote = __ballot_sync(0xffffffffu, begins);
-  if (lane == 0) count_s[warp] = __popc(vote);
-  __syncthreads();
-  int rank = __popc(vote & ((1u << lane) - 1u));
-  for (int w = 0; w < warp; ++w) rank += count_s[w];
-  if (begins && rank == static_cast<int>(blockIdx.y)) c0_s = tid + 1;
-  __syncthreads();
-  const int c0 = c0_s;
-  if (c0 == 0) return;
-  const int row = __ldcg(p.first_row + c0);
-  const int n = 1 + __syncthreads_count(c0 + tid < ctas && __ldcg(p.first_row + c0 + tid) == row);   // partials
+  const int2 cut = __ldcg(p.cut + c0);
+  const int row = cut.x, n = cut.y;
+  if (n == 0) return;
   if (tid < n) slot_s[tid] = tid == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + tid - 1);
   __syncthreads();
-  // every warp: joint maximum; thread i: the factor of partial i
+  // every warp: joint maximum and sum of its head, and the partials' factors
   const float2* ml = reinterpret_cast<const float2*>(p.ml) + h;
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(ml + slot_s[i] * 64).x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if (tid < n) w_s[tid] = M == -INFINITY ? 0.0f : exp2f(__ldcg(ml + slot_s[tid] * 64).x - M);
-  __syncthreads();
   float L = 0.0f;
-  for (int i = lane; i < n; i += 32) L += w_s[i] * __ldcg(ml + slot_s[i] * 64).y;
+  for (int i = lane; i < n; i += 32) {
+    const float2 v = __ldcg(ml + slot_s[i] * 64);
+    const float f = M == -INFINITY ? 0.0f : exp2f(v.x - M);
+    L += f * v.y;
+    if ((warp & 3) == 0) w_s[g][i] = f;
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-  const int g = tid >> 7, t = tid & 127;
+  __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const float4* op = reinterpret_cast<const float4*>(p.opart + static_cast<int64_t>(h) * 512) + t;
-#pragma unroll 8
-  for (int i = g; i < n; i += 4) {
-    const float4 o = __ldcg(op + static_cast<int64_t>(slot_s[i]) * (64 * 512 / 4));
-    const float f = w_s[i];
-    acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
-  }
-  if (g > 0) acc_s[g - 1][t] = acc;
-  __syncthreads();
-  if (g > 0) return;
+  constexpr int kStep = SPLIT ? 4 : 1;
+  for (int i = SPLIT ? g : 0; i < n; i += 4 * kStep) {
+    // behind the last partial: the last one again, with factor 0
+    float4 o[4];
+    float f[4];
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const float4 o = acc_s[k][t];
-    acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+    for (int j = 0; j < 4; ++j) {
+      const int k = i + j * kStep, kc = min(k, n - 1);
+      o[j] = __ldcg(op + static_cast<int64_t>(slot_s[kc]) * (64 * 512 / 4));
+      f[j] = k < n ? w_s[g][kc] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc.x += f[j] * o[j].x; acc.y += f[j] * o[j].y; acc.z += f[j] * o[j].z; acc.w += f[j] * o[j].w;
+    }
+  }
+  if (SPLIT) {
+    if (g > 0) acc_s[g - 1][t] = acc;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const float4 o = acc_s[k][t];
+      acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+    }
   }
   const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
   uint2 packed;
