@@ -348,7 +348,8 @@ def csa2_stack_decode_io(args, io, ws, stream=None):
 
 def _need(t, what, dtype, *shape):
     """A dense tensor of this type and shape (None: any size)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.dtype != dtype or (t.shape != shape and (t.dim() != len(shape) or
+                                                  any(n is not None and n != m for n, m in zip(shape, t.shape)))):
         raise ValueError(f"{what}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
@@ -365,20 +366,33 @@ def _need_table(block_table, B):
 
 
 def _one_device(tensors):
-    """All given tensors on one device; its index."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
-    return devices.pop()
+    """All given tensors on one device; that device."""
+    device = None
+    for t in tensors:
+        if t is not None and t.device != device:
+            if device is not None:
+                raise ValueError(f"tensors on several devices: {device}, {t.device}")
+            device = t.device
+    return device
 
 
-def _on_device(device, ws=None):
-    """Makes the tensors' device current for a call (the library launches on the current device)."""
+def _launch(call, what, device, stream, *args):
+    """call(*args, stream) with the tensors' device current (the library
+    launches on the current device)."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {device}")
-    if ws is not None and ws.device != device:
-        raise ValueError(f"workspace on {ws.device}, tensors on {device}")
-    return torch.cuda.device(device)
+    if torch._C._cuda_getDevice() != device.index:
+        with torch.cuda.device(device):
+            return _launch(call, what, device, stream, *args)
+    status = call(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    if status != 0:
+        _check(status, what)
+
+
+def _launch_ws(call, what, a, ws, stream):
+    if ws.device != a._device:
+        raise ValueError(f"workspace on {ws.device}, tensors on {a._device}")
+    _launch(call, what, a._device, stream, ctypes.byref(a), ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def block_table_args(len, n_new, free_blocks, block_table, slots, start, len_out, info, block_size, free_pos=None):
@@ -405,9 +419,7 @@ def block_table_args(len, n_new, free_blocks, block_table, slots, start, len_out
 
 def csa2_block_tables(args, ws, stream=None):
     """Block tables, pool rows and lengths of one step (see csa2.h)."""
-    with _on_device(args._device, ws):
-        _check(load().csa2_block_tables(ctypes.byref(args), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-               "csa2_block_tables")
+    _launch_ws(load().csa2_block_tables, "csa2_block_tables", args, ws, stream)
 
 
 def csa2_paged_rows(positions, block_table, rows, block_size, n_blocks, n_vis=None, stream=None):
@@ -420,10 +432,10 @@ def csa2_paged_rows(positions, block_table, rows, block_size, n_blocks, n_vis=No
     _need(rows, "rows", torch.int32, B, Q, K)
     if n_vis is not None:
         _need(n_vis, "n_vis", torch.int32, B, Q)
-    a = PagedRowsArgs(B=B, Q=Q, K=K, block_size=block_size, max_blocks=max_blocks, ld_table=ld, n_blocks=n_blocks,
-                      positions=_ptr(positions), n_vis=_ptr(n_vis), block_table=_ptr(block_table), rows=_ptr(rows))
-    with _on_device(_one_device((positions, block_table, rows, n_vis))):
-        _check(load().csa2_paged_rows(ctypes.byref(a), _stream(stream)), "csa2_paged_rows")
+    a = PagedRowsArgs(B, Q, K, block_size, max_blocks, ld, n_blocks, positions.data_ptr(),
+                      None if n_vis is None else n_vis.data_ptr(), block_table.data_ptr(), rows.data_ptr())
+    _launch(load().csa2_paged_rows, "csa2_paged_rows", _one_device((positions, block_table, rows, n_vis)), stream,
+            ctypes.byref(a))
 
 
 def paged_attn_args(q, kv, block_table, n_vis, out, lse=None, swa=None, W=0, swa_step=0, swa_scale=None, scale=0.0):
@@ -464,9 +476,7 @@ def paged_attn_args(q, kv, block_table, n_vis, out, lse=None, swa=None, W=0, swa
 
 def csa2_paged_attn(args, ws, stream=None):
     """Attention over all visible entries of a paged cache (see csa2.h)."""
-    with _on_device(args._device, ws):
-        _check(load().csa2_paged_attn(ctypes.byref(args), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-               "csa2_paged_attn")
+    _launch_ws(load().csa2_paged_attn, "csa2_paged_attn", args, ws, stream)
 
 
 def csa2_workspace_size(args, which):
