@@ -179,12 +179,21 @@ __device__ __forceinline__ const uint8_t* paged_row(const PagedAttnParams& p, co
 // Wait of a whole warp.  Every lane polls: with one lane polling for the
 // others, the warp could go on in two parts, and what all lanes must execute
 // together (tcgen05, named barriers) then happened twice.
-__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, int err, volatile int* abort) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+__device__ __forceinline__ bool paged_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, int err, volatile int* abort) {
+  if (__all_sync(0xffffffffu, paged_try_wait(bar, parity))) return true;
   // bounded by polls, which take some 140 cycles each: a second or two
 #pragma unroll 1
   for (uint32_t n = 0; n < kPagedPolls && !*abort; ++n)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, paged_try_wait(bar, parity))) return true;
   __syncwarp();
   if (!*abort) {
     record_error(err);
@@ -193,10 +202,13 @@ __device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, int e
   __syncwarp();
   return false;
 }
-__device__ __forceinline__ void paged_arrive(uint64_t* bar) {
+__device__ __forceinline__ void paged_arrive(uint32_t bar) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
   __syncwarp();
+}
+__device__ __forceinline__ void paged_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ void paged_bar(int id, int nthreads) {
   __syncwarp();
@@ -256,6 +268,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Waits for tensor-memory loads; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void paged_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
 }
 // umma_bf16 with the descriptors' high words apart: only the low ones (the
 // addresses) change from one MMA to the next.
@@ -343,17 +361,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t pt = qt + kTcQTileBytes;
   const uint32_t misc32 = pt + kTcPTileBytes;
   uint8_t* misc = smem + kTcKeyTileBytes + kTcQTileBytes + kTcPTileBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
-  uint64_t* full = bars;                                // [4] slab filled (4 loader warps)
-  uint64_t* freed = bars + 4;                           // [4] slab read by MMA 2
-  uint64_t* q_full = bars + 8;
-  uint64_t* s_full = bars + 9;                          // MMA 1 done (and every MMA before it)
-  uint64_t* p_full = bars + 10;                         // P^T written, O^T rescaled (16 softmax warps)
-  uint64_t* o_full = bars + 11;                         // the query part's last MMA 2 done
-  uint64_t* q_tma = bars + 12;                          // Q arrived, in natural order (FP4 pools)
-  uint64_t* q_free = bars + 13;                         // the query part's last MMA 1 done
-  uint64_t* rows_full = bars + 14;                      // [3] row addresses written
-  uint64_t* rows_free = bars + 17;                      // [3] ... and the tile's last MMA 2 done
+  const uint32_t full = misc32;                         // [4] slab filled (4 loader warps)
+  const uint32_t freed = misc32 + 32;                   // [4] slab read by MMA 2
+  const uint32_t q_full = misc32 + 64;
+  const uint32_t s_full = misc32 + 72;                  // MMA 1 done (and every MMA before it)
+  const uint32_t p_full = misc32 + 80;                  // P^T written, O^T rescaled (16 softmax warps)
+  const uint32_t o_full = misc32 + 88;                  // the query part's last MMA 2 done
+  const uint32_t q_tma = misc32 + 96;                   // Q arrived, in natural order (FP4 pools)
+  const uint32_t q_free = misc32 + 104;                 // the query part's last MMA 1 done
+  const uint32_t rows_full = misc32 + 112;              // [3] row addresses written
+  const uint32_t rows_free = misc32 + 136;              // [3] ... and the tile's last MMA 2 done
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 164);
   const uint32_t kind_s = misc32 + 176;                               // int [3]
@@ -367,14 +384,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 32) {
-    for (int i = 0; i < 4; ++i) { mbar_init(&full[i], kPagedLoaders / 2); mbar_init(&freed[i], 1); }
-    mbar_init(q_full, KVB ? 1 : kPagedQWarps);
-    mbar_init(q_tma, 1);
-    mbar_init(q_free, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, kPagedSoftmax);
-    mbar_init(o_full, 1);
-    for (int i = 0; i < kPagedStages; ++i) { mbar_init(&rows_full[i], 1); mbar_init(&rows_free[i], 1); }
+    uint64_t* bars = reinterpret_cast<uint64_t*>(misc);  // in the order above
+    for (int i = 0; i < 20; ++i)
+      mbar_init(bars + i, i < 4 ? kPagedLoaders / 2 : i == 8 ? (KVB ? 1 : kPagedQWarps) : i == 10 ? kPagedSoftmax : 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
@@ -424,7 +436,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           uint32_t da = static_cast<uint32_t>(kd), db = static_cast<uint32_t>(qd);
 #pragma unroll 1
           for (int t = 0; t < 4; ++t) {
-            ok = paged_wait(&full[t], ph, kErrWaitTmaFull, abort_flag) && ok;
+            ok = paged_wait(full + 8 * t, ph, kErrWaitTmaFull, abort_flag) && ok;
             tc_fence_after();
             if (ok && issuer) {
 #pragma unroll
@@ -437,8 +449,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             db += 2 * 8192 >> 4;
           }
           if (issuer) {
-            umma_commit(s_full);
-            if (last) umma_commit(q_free);
+            paged_commit(s_full);
+            if (last) paged_commit(q_free);
           }
           __syncwarp();
           const bool more = paged_next(p, c), next_last = c.t + 1 == c.t1;
@@ -453,13 +465,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
                 paged_mma(tmem + 64 + 64 * t, da + (kk * 2048 >> 4), vd >> 32, static_cast<uint32_t>(pd) + (kk * 2048 >> 4), pd >> 32,
                           idesc2, (!first || kk > 0) ? 1u : 0u);
             }
-            if (issuer) umma_commit(&freed[t]);
+            if (issuer) paged_commit(freed + 8 * t);
             __syncwarp();
             da += 2 * 16384 >> 4;
           }
           if (issuer) {
-            umma_commit(&rows_free[stage]);
-            if (last) umma_commit(o_full);
+            paged_commit(rows_free + 8 * stage);
+            if (last) paged_commit(o_full);
           }
           __syncwarp();
           if (!more) break;
@@ -475,7 +487,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         int stage = 0;
         uint32_t ph = 1;
         while (true) {
-          paged_wait(&rows_free[stage], ph, kErrWaitSmemEmpty, abort_flag);
+          paged_wait(rows_free + 8 * stage, ph, kErrWaitSmemEmpty, abort_flag);
           const bool window = c.t >= c.kv_tiles;
           const int b = c.row / p.Q;
           const int key0 = (window ? c.t - c.kv_tiles : c.t) * kPagedKeys + lane;
@@ -498,7 +510,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               for (int o = 0; o < bytes; o += 128) prefetch_l2(row + o);
           }
           if (lane == 0) sts(kind_s + 4 * stage, window ? (p.swa_fp8 ? kPagedFp8 : kPagedBf16) : kPagedPool);
-          paged_arrive(&rows_full[stage]);
+          paged_arrive(rows_full + 8 * stage);
           if (!paged_next(p, c)) break;
           if (++stage == kPagedStages) { stage = 0; ph ^= 1; }
         }
@@ -508,7 +520,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         for (uint32_t part = 0;; ++part) {
           paged_wait(q_free, (part & 1) ^ 1, kErrWaitOperand, abort_flag);
           if (qtid == 0) {
-            uint64_t* arrived = KVB ? q_full : q_tma;
+            uint64_t* arrived = reinterpret_cast<uint64_t*>(misc + (KVB ? 64 : 96));   // q_full or q_tma
             mbar_arrive_expect_tx(arrived, kTcQTileBytes);
             const uint64_t pol = l2_policy_evict_first();
             for (int k = 0; k < 8; ++k) tma_load_2d(smem + kTcKeyTileBytes + k * 8192, &tmap_q, arrived, 64 * k, c.row * 64, pol);
@@ -566,9 +578,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
       };
       auto publish = [&](int t) {
         fence_async_smem();
-        paged_arrive(&full[t]);
+        paged_arrive(full + 8 * t);
       };
-      paged_wait(&rows_full[0], 0, kErrWaitOperand, abort_flag);
+      paged_wait(rows_full + 8 * 0, 0, kErrWaitOperand, abort_flag);
       fetch(0);
       int stage = 0;
       uint32_t ph_rows = 0;
@@ -578,7 +590,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           uint32_t chunk = kt + (2 * t0 + (u >> 1)) * 16384 + sw128_off(key0 + kk, 4 * (u & 1));
 #pragma unroll 1
           for (int t = t0; t < 4; t += 2) {
-            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
+            paged_wait(freed + 8 * t, ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const __nv_bfloat162 sc = paged_scales(rsc[0][i]);
@@ -603,7 +615,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int t = t0 + 2 * k;
-            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
+            paged_wait(freed + 8 * t, ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint8_t* src = row[i] ? row[i] + 256 * t + 16 * (lane & 7) : p.kv;
@@ -623,7 +635,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           const bool fp8 = kind == kPagedFp8;
 #pragma unroll 1
           for (int t = t0; t < 4; t += 2) {
-            paged_wait(&freed[t], ph, kErrWaitSmemEmpty, abort_flag);
+            paged_wait(freed + 8 * t, ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll 1
             for (int i = 0; i < 8; i += 2) {
               const uint8_t* row[2];
@@ -661,7 +673,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         }
         if (--left == 0) break;
         if (++stage == kPagedStages) { stage = 0; ph_rows ^= 1; }
-        paged_wait(&rows_full[stage], ph_rows, kErrWaitOperand, abort_flag);
+        paged_wait(rows_full + 8 * stage, ph_rows, kErrWaitOperand, abort_flag);
         fetch(stage);                                   // behind the tile's last fence, which would wait for the loads
       }
     } else {
@@ -683,7 +695,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           paged_bar(bar, 128);
         }
         const bool window = c.t >= c.kv_tiles;
-        paged_wait(&full[0], it & 1, kErrWaitSmemEmpty, abort_flag);      // a loader has seen the tile's addresses
+        paged_wait(full + 8 * 0, it & 1, kErrWaitSmemEmpty, abort_flag);      // a loader has seen the tile's addresses
         const bool there = lds_ptr(row_s + 8 * (stage * 128 + key)) != nullptr;
         float rs = (window && p.swa_fp8) ? lds_f(wsc_s + 4 * (stage * 128 + key)) : 1.0f;
         if (++stage == kPagedStages) stage = 0;
@@ -700,14 +712,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         auto weights = [&]() {
           uint32_t r[16];
           tmem_ld_32x32b_x16(tmem + lanes + head0, r);
-          tmem_ld_wait();
+          float4 nr[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) nr[j] = lds_f4(nref_s + 4 * (head0 + 4 * j));
+          paged_ld_wait(r);
 #pragma unroll
           for (int j = 0; j < 16; j += 4) {
-            const float4 nr = lds_f4(nref_s + 4 * (head0 + j));
-            y[j] = fmaf(__uint_as_float(r[j]), ls, nr.x);
-            y[j + 1] = fmaf(__uint_as_float(r[j + 1]), ls, nr.y);
-            y[j + 2] = fmaf(__uint_as_float(r[j + 2]), ls, nr.z);
-            y[j + 3] = fmaf(__uint_as_float(r[j + 3]), ls, nr.w);
+            y[j] = fmaf(__uint_as_float(r[j]), ls, nr[j / 4].x);
+            y[j + 1] = fmaf(__uint_as_float(r[j + 1]), ls, nr[j / 4].y);
+            y[j + 2] = fmaf(__uint_as_float(r[j + 2]), ls, nr[j / 4].z);
+            y[j + 3] = fmaf(__uint_as_float(r[j + 3]), ls, nr[j / 4].w);
           }
           if (!__all_sync(0xffffffffu, there)) {
 #pragma unroll
@@ -736,7 +750,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             float v[16];
             uint32_t r[16];
             tmem_ld_32x32b_x16(tmem + lanes + head0, r);
-            tmem_ld_wait();
+            paged_ld_wait(r);
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = there ? __uint_as_float(r[j]) * ls : -INFINITY;
             const float m = warp_reduce_heads16<true>(v, lane);
@@ -765,7 +779,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               uint32_t r[16];
               const uint32_t ta = tmem + lanes + 64 + 64 * t + head0;
               tmem_ld_32x32b_x16(ta, r);
-              tmem_ld_wait();
+              paged_ld_wait(r);
 #pragma unroll
               for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * lds_f(fac_s + 4 * (head0 + j)));
               tmem_st_32x32b_x16(ta, r);
@@ -827,7 +841,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           for (int t = 0; t < 4; ++t) {
             uint32_t r[16];
             tmem_ld_32x32b_x16(tmem + lanes + 64 + 64 * t + head0, r);
-            tmem_ld_wait();
+            paged_ld_wait(r);
             const int d = 128 * t + 32 * quarter + ch;
             if (whole) {
               // lanes pair up: the even one writes dims d, d + 1 of head j, the odd one of head j + 1
