@@ -169,8 +169,9 @@ csa2_status device_info(DeviceInfo** out) {
         set_smem_attrs(paged_rows_kernel, 0) != cudaSuccess ||
         set_smem_attrs(paged_attn_kernel<false>, static_cast<int>(kPagedSmem)) != cudaSuccess ||
         set_smem_attrs(paged_attn_kernel<true>, static_cast<int>(kPagedSmem)) != cudaSuccess ||
-        set_smem_attrs(paged_attn_join_kernel<true>, 0) != cudaSuccess ||
-        set_smem_attrs(paged_attn_join_kernel<false>, 0) != cudaSuccess)
+        set_smem_attrs(paged_attn_join_kernel<2>, 0) != cudaSuccess ||
+        set_smem_attrs(paged_attn_join_kernel<1>, 0) != cudaSuccess ||
+        set_smem_attrs(paged_attn_join_kernel<0>, 0) != cudaSuccess)
       return CSA2_ERR_CUDA;
     d.topk_max_cluster = topk_cluster_limit();
     if (!g_encode) {
@@ -706,10 +707,9 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   if (e != cudaSuccess) return CSA2_ERR_CUDA;
   if (ctas == 1) return CSA2_OK;                       // no range boundary
   trace_pre(kKPagedJoin, st);
-  // a cut query has (CTAs + queries) / queries partials or so
-  const bool split = p.BQ <= kPagedSplitJoin;
-  e = launch_ex(split ? paged_attn_join_kernel<true> : paged_attn_join_kernel<false>,
-                split ? dim3(64, static_cast<unsigned>(std::min(p.BQ, ctas - 1))) : dim3(16, static_cast<unsigned>(ctas - 1)),
+  const int split = p.BQ > kPagedSplitJoin ? 0 : p.BQ > kPagedHalfJoin ? 1 : 2;
+  e = launch_ex(split == 2 ? paged_attn_join_kernel<2> : split == 1 ? paged_attn_join_kernel<1> : paged_attn_join_kernel<0>,
+                split ? dim3(64 * split, static_cast<unsigned>(std::min(p.BQ, ctas - 1))) : dim3(16, static_cast<unsigned>(ctas - 1)),
                 dim3(kPagedJoinThreads), 0, st, 0, p, ctas);
   trace_post(st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;

@@ -878,22 +878,33 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 // 2(c-1)+1, 2c, 2(c+1), ...; cut[c] names it and counts them.  Partials are
 // added in a fixed order whatever the timing.
 //
-// SPLIT (few queries, many partials each): CTA (h, y) takes head h of the
-// y-th cut query, its four thread groups every fourth partial each.  Else
-// (many queries, few partials each): CTA (x, y) takes boundary y + 1, if a
-// query is first cut there, and its four groups one head each.
-// 128 threads x 4 dims per group, four 16-byte loads in flight.
+// SPLIT = 0 (many queries, few partials each): CTA (x, y) takes boundary
+// y + 1, if a query is first cut there, and its four groups of 128 threads one
+// head each.  SPLIT = 1 (fewer queries): CTA (h, y) takes head h of the y-th
+// cut query, its four groups every fourth partial each.  SPLIT = 2 (one query
+// or two): CTA (x, y) takes half of head x / 2's dims, its eight groups of 64
+// threads every eighth partial each.  A thread owns 4 dims and keeps kFlight
+// 16-byte loads in flight, the first of them over the reading of maxima and
+// sums: the chain of dependent reads bounds the kernel, not the bytes.
+//
+// Where the rule lies, attention and join of 262,144 entries in all (us):
+//   queries      1     2     4     8    12    16    20
+//   SPLIT 2   69.7  68.2  69.7  76.5  84.7  90.8  97.1
+//   SPLIT 1   72.4  69.1  66.8  69.9  76.2  79.1  82.7
+//   SPLIT 0  117.6  91.4  79.6  73.9  75.6  75.3  75.3
 constexpr int kPagedJoinThreads = 512;
-constexpr int kPagedSplitJoin = 16;                    // up to this many queries SPLIT
-template <bool SPLIT>
+constexpr int kPagedHalfJoin = 2, kPagedSplitJoin = 10;            // queries up to which SPLIT is 2, 1
+template <int SPLIT>
 __global__ void __launch_bounds__(kPagedJoinThreads)
 paged_attn_join_kernel(PagedAttnParams p, int ctas) {
   __shared__ int c0_s, count_s[kPagedJoinThreads / 32];
   __shared__ int slot_s[kPagedMaxCtas + 1];              // slot of each partial
-  __shared__ float w_s[4][kPagedMaxCtas + 1];            // and its factor, per head of the CTA
-  __shared__ float4 acc_s[3][128];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = tid >> 7, t = tid & 127;
-  const int h = SPLIT ? blockIdx.x : 4 * blockIdx.x + g;
+  __shared__ float w_s[SPLIT ? 1 : 4][kPagedMaxCtas + 1];  // and its factor, per head of the CTA
+  constexpr int kGroup = SPLIT == 2 ? 64 : 128, kGroups = kPagedJoinThreads / kGroup, kFlight = SPLIT ? 8 : 4;
+  __shared__ float4 acc_s[SPLIT ? kGroups - 1 : 1][kGroup];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = tid / kGroup, t = tid % kGroup;
+  const int h = SPLIT ? blockIdx.x / SPLIT : 4 * blockIdx.x + g;
+  const int d = SPLIT == 2 ? 4 * (t + kGroup * (blockIdx.x & 1)) : 4 * t;     // first of the thread's dims
   pdl_launch_dependents();
   if (SPLIT && tid == 0) c0_s = 0;
   pdl_wait();
@@ -915,56 +926,67 @@ paged_attn_join_kernel(PagedAttnParams p, int ctas) {
   if (n == 0) return;
   if (tid < n) slot_s[tid] = tid == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + tid - 1);
   __syncthreads();
+  const float* op = p.opart + static_cast<int64_t>(h) * 512 + d;
+  constexpr int kStep = SPLIT ? kGroups : 1;
+  int i = SPLIT ? g : 0;
+  float4 o[kFlight];
+#pragma unroll
+  for (int j = 0; j < kFlight; ++j)                     // behind the last partial: the last one again, with factor 0
+    o[j] = __ldcg(reinterpret_cast<const float4*>(op + static_cast<int64_t>(slot_s[min(i + j * kStep, n - 1)]) * (64 * 512)));
   // every warp: joint maximum and sum of its head, and the partials' factors
   const float2* ml = reinterpret_cast<const float2*>(p.ml) + h;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(ml + slot_s[i] * 64).x);
+  constexpr int kMl = (kPagedMaxCtas + 1 + 31) / 32;
+  float2 v[kMl];
+  float M = -INFINITY, L = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kMl; ++j) {
+    v[j] = make_float2(-INFINITY, 0.0f);
+    if (lane + 32 * j < n) v[j] = __ldcg(ml + slot_s[lane + 32 * j] * 64);
+  }
+#pragma unroll
+  for (int j = 0; j < kMl; ++j) M = fmaxf(M, v[j].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  float L = 0.0f;
-  for (int i = lane; i < n; i += 32) {
-    const float2 v = __ldcg(ml + slot_s[i] * 64);
-    const float f = M == -INFINITY ? 0.0f : exp2f(v.x - M);
-    L += f * v.y;
-    if ((warp & 3) == 0) w_s[g][i] = f;
+#pragma unroll
+  for (int j = 0; j < kMl; ++j) {
+    const float f = M == -INFINITY ? 0.0f : exp2f(v[j].x - M);
+    L += f * v[j].y;
+    if (t < 32 && lane + 32 * j < n) w_s[SPLIT ? 0 : g][lane + 32 * j] = f;        // (SPLIT: the groups write the same)
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
   __syncthreads();
+  const float* w = w_s[SPLIT ? 0 : g];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* op = reinterpret_cast<const float4*>(p.opart + static_cast<int64_t>(h) * 512) + t;
-  constexpr int kStep = SPLIT ? 4 : 1;
-  for (int i = SPLIT ? g : 0; i < n; i += 4 * kStep) {
-    // behind the last partial: the last one again, with factor 0
-    float4 o[4];
-    float f[4];
+  while (true) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = i + j * kStep, kc = min(k, n - 1);
-      o[j] = __ldcg(op + static_cast<int64_t>(slot_s[kc]) * (64 * 512 / 4));
-      f[j] = k < n ? w_s[g][kc] : 0.0f;
+    for (int j = 0; j < kFlight; ++j) {
+      const int k = i + j * kStep;
+      const float f = k < n ? w[k] : 0.0f;
+      acc.x += f * o[j].x; acc.y += f * o[j].y; acc.z += f * o[j].z; acc.w += f * o[j].w;
     }
+    i += kFlight * kStep;
+    if (i >= n) break;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      acc.x += f[j] * o[j].x; acc.y += f[j] * o[j].y; acc.z += f[j] * o[j].z; acc.w += f[j] * o[j].w;
-    }
+    for (int j = 0; j < kFlight; ++j)
+      o[j] = __ldcg(reinterpret_cast<const float4*>(op + static_cast<int64_t>(slot_s[min(i + j * kStep, n - 1)]) * (64 * 512)));
   }
   if (SPLIT) {
     if (g > 0) acc_s[g - 1][t] = acc;
     __syncthreads();
     if (g > 0) return;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const float4 o = acc_s[k][t];
-      acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+    for (int k = 0; k < kGroups - 1; ++k) {
+      const float4 q = acc_s[k][t];
+      acc.x += q.x; acc.y += q.y; acc.z += q.z; acc.w += q.w;
     }
   }
   const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
   uint2 packed;
   packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(row) * 64 + h) * 512 + 4 * t) = packed;
-  if (p.lse && t == 0)
+  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(row) * 64 + h) * 512 + d) = packed;
+  if (p.lse && d == 0)
     p.lse[static_cast<int64_t>(row) * 64 + h] = (L > 0.0f) ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
