@@ -589,6 +589,7 @@ csa2_status run_block_tables(const csa2_block_table_args* a, void* ws, cudaStrea
   TablesParams t;
   t.B = a->B;
   t.P = static_cast<uint32_t>(a->block_size);
+  t.by_P = DivBy::of(t.P);
   t.cap = static_cast<int64_t>(a->block_size) * a->max_blocks;
   t.ld_table = a->ld_table;
   t.len = a->len; t.n_new = a->n_new; t.free_blocks = a->free_blocks; t.n_free = a->n_free; t.free_pos = a->free_pos;
@@ -626,7 +627,8 @@ csa2_status run_paged_rows(const csa2_paged_rows_args* a, cudaStream_t st) {
   PagedRowsParams p;
   p.pos = a->positions; p.n_vis = a->n_vis; p.table = a->block_table; p.rows = a->rows;
   p.n = static_cast<uint32_t>(a->B) * a->Q * a->K;
-  p.K = a->K; p.Q = a->Q; p.P = a->block_size;
+  p.by_K = DivBy::of(a->K); p.by_Q = DivBy::of(a->Q); p.by_P = DivBy::of(a->block_size);
+  p.P = a->block_size;
   p.max_blocks = a->max_blocks; p.n_blocks = static_cast<uint32_t>(a->n_blocks);
   p.ld_table = a->ld_table;
   trace_pre(kKPagedRows, st);
