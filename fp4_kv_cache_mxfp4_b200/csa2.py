@@ -357,12 +357,12 @@ def _need(t, what, dtype, *shape):
 
 def _need_table(block_table, B):
     """(max_blocks, ld_table) of an int32 [B, max_blocks] table whose rows may lie apart."""
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected torch.int32 [{B}, max_blocks], got {block_table.dtype} "
-                         f"{list(block_table.shape)}")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    shape, strides = block_table.shape, block_table.stride()
+    if block_table.dtype != torch.int32 or len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table: expected torch.int32 [{B}, max_blocks], got {block_table.dtype} {list(shape)}")
+    if shape[1] > 1 and strides[1] != 1:
         raise ValueError("block_table: the entries of a row must be contiguous")
-    return block_table.shape[1], block_table.stride(0) if B > 1 else block_table.shape[1]
+    return shape[1], strides[0] if B > 1 else shape[1]
 
 
 def _one_device(tensors):
