@@ -24,12 +24,21 @@
 // (M = 128 dims x 4, N = 64, K = 128 keys) with the same bf16 key tile read
 // along its other axis.
 //
-// What bounds it: 64 MMA instructions per tile, each reading 6 KB of operands
-// from shared memory at 128 B per cycle, 48 cycles (measured), so 3072 cycles
-// per tile: 2.7 MMAC of a possible 4.1 per cycle.  One key tile (128 KB), Q (64 KB)
-// and P^T (16 KB) fill the shared memory, so the tile is filled in slabs of
-// 128 dims: MMA 2 releases slab t when its output rows t are done, and the
-// next tile's slab t is expanded while MMA 2 runs on the others.  Roles:
+// What bounds it: the data path of shared memory and L1, 128 B per cycle.  A
+// tile's 64 MMAs read 6 KB of operands each, 48 cycles (measured; the MMA rate
+// alone would allow 32), 3072 per tile; expanded keys are written at 1024, raw
+// ones pass at some 550.  One key tile (128 KB), Q (64 KB) and P^T (16 KB)
+// fill the shared memory, so there is no second tile to work on while the
+// softmax runs (some 1300 cycles, 512 of them the exponentials' rate); the
+// tile is filled in slabs of 128 dims instead: MMA 2 releases slab t when its
+// output rows t are done, and the next tile's slab t is expanded while MMA 2
+// runs on the others.  Measured, a tile takes some 6000 cycles: MMA 2 2250,
+// MMA 1 2450, softmax 1300.  Four sequences of 131,072 entries take 110 us (42 at
+// the bf16 rate), one of 1,048,576 203 us (84), both with the join.
+// Tried and slower: a second issuing warp for MMA 1 (its MMAs and MMA 2's
+// then took 100 cycles each, 10 % in all), whole or half slabs expanded
+// before the wait for their place (7 and 4 %), one lane or one warp polling
+// for the others (11 and 1 %).  Roles:
 //   warp 0       MMA issue (the scheduler prefers older warps: as the last warp
 //                it lost hundreds of cycles per tile to the loaders)
 //   warp 1       row addresses of the tiles to come (block table, window),
@@ -39,10 +48,10 @@
 //                wait in registers; bf16 rows go by cp.async)
 //   warps 12-27  softmax: S^T from tensor memory, weights to P^T, and the
 //                epilogue; warp w has keys 32 (w % 4).. and heads 16 (w / 4 - 3)..
-// Every role fits in the 72 registers that 28 warps leave each thread: with
-// the whole shared memory taken, L1 is too small for spilled values to stay,
-// and each reload then costs an L2 round trip (a version with some twenty
-// spilled registers took 1.5 times as long).
+// Every role about fits in the 72 registers that 28 warps leave each thread
+// (24 bytes are spilled; none with 80 for a loader, 2 % slower): with the whole
+// shared memory taken, L1 is too small for spilled values to stay, and each
+// reload then costs an L2 round trip.
 //
 // FP4 to bf16 in 9 logic, 4 multiply-add and 4 half-precision instructions
 // per 8 channels (the ALU rate, half the FMA rate, is what bounds the
@@ -370,7 +379,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t q_tma = misc32 + 96;                   // Q arrived, in natural order (FP4 pools)
   const uint32_t q_free = misc32 + 104;                 // the query part's last MMA 1 done
   const uint32_t rows_full = misc32 + 112;              // [3] row addresses written
-  const uint32_t rows_free = misc32 + 136;              // [3] ... and the tile's last MMA 2 done
+  const uint32_t rows_free = misc32 + 136;              // [3] ... and read (16 softmax warps)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 164);
   const uint32_t kind_s = misc32 + 176;                               // int [3]
@@ -386,7 +395,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   if (tid == 32) {
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc);  // in the order above
     for (int i = 0; i < 20; ++i)
-      mbar_init(bars + i, i < 4 ? kPagedLoaders / 2 : i == 8 ? (KVB ? 1 : kPagedQWarps) : i == 10 ? kPagedSoftmax : 1);
+      mbar_init(bars + i, i < 4 ? kPagedLoaders / 2 : i == 8 ? (KVB ? 1 : kPagedQWarps) : i == 10 || i >= 17 ? kPagedSoftmax : 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
@@ -416,7 +425,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         // issue slots among busy warps.
         const bool issuer = elect_one() && lane == 0;
         uint32_t ph_q = 0;
-        int stage = 0;
         bool first = true;
         // descriptors of the tiles' first bytes; an offset adds to the 16-byte address field
         const uint64_t kd = umma_desc_sw128_kmajor(kt), qd = umma_desc_sw128_kmajor(qt);
@@ -469,15 +477,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             __syncwarp();
             da += 2 * 16384 >> 4;
           }
-          if (issuer) {
-            paged_commit(rows_free + 8 * stage);
-            if (last) paged_commit(o_full);
-          }
+          if (issuer && last) paged_commit(o_full);
           __syncwarp();
           if (!more) break;
           first = last;
           last = next_last;
-          if (++stage == kPagedStages) stage = 0;
         }
         paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
         tc_fence_after();
@@ -698,7 +702,6 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         paged_wait(full + 8 * 0, it & 1, kErrWaitSmemEmpty, abort_flag);      // a loader has seen the tile's addresses
         const bool there = lds_ptr(row_s + 8 * (stage * 128 + key)) != nullptr;
         float rs = (window && p.swa_fp8) ? lds_f(wsc_s + 4 * (stage * 128 + key)) : 1.0f;
-        if (++stage == kPagedStages) stage = 0;
         const float ls = p.scale_log2 * (KVB || window ? rs : kPagedFp4Up);
         if (!KVB && window) rs *= kPagedFp4Down;
         paged_wait(s_full, it & 1, kErrWaitTmemFull, abort_flag);
@@ -790,6 +793,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         }
         tc_fence_before();
         paged_arrive(p_full);
+        // (the loaders are through with the addresses too; a tcgen05.commit for
+        // this would hold the MMA warp up until its queue has drained)
+        paged_arrive(rows_free + 8 * stage);
+        if (++stage == kPagedStages) stage = 0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) sum[j] += y[j];    // unrounded: the log-sum-exp keeps float32
         first = false;
