@@ -686,6 +686,7 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   p.BQ = a->B * a->Q; p.Q = a->Q; p.W = a->W;
   p.w_tiles = (a->W + kPagedKeys - 1) / kPagedKeys;
   p.block_size = a->block_size; p.max_blocks = a->max_blocks;
+  p.by_block = DivBy::of(p.block_size);
   p.ld_table = a->ld_table; p.n_blocks = a->n_blocks; p.block_stride = a->block_stride;
   p.kv = static_cast<const uint8_t*>(a->kv);
   p.table = a->block_table; p.n_vis = a->n_vis;

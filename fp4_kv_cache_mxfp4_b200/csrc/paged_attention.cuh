@@ -94,6 +94,7 @@ struct PagedAttnParams {
   int BQ, Q, W;
   int w_tiles;               // ceil(W / 128)
   uint32_t block_size, max_blocks;
+  DivBy by_block;
   int64_t ld_table, n_blocks, block_stride;            // block_stride in bytes
   const uint8_t* kv;
   const int32_t* table;
@@ -179,7 +180,7 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedCursor
 // Address of entry `pos` of a request's cache; nullptr where the table names no block of the pool.
 __device__ __forceinline__ const uint8_t* paged_row(const PagedAttnParams& p, const int32_t* table, uint32_t pos,
                                                     uint32_t row_bytes) {
-  const uint32_t blk = pos / p.block_size;
+  const uint32_t blk = p.by_block(pos);
   const int32_t id = table[blk];
   if (id < 0 || id >= p.n_blocks) return nullptr;
   return p.kv + id * p.block_stride + static_cast<int64_t>(pos - blk * p.block_size) * row_bytes;
