@@ -712,7 +712,7 @@ csa2_status run_paged_attn(const csa2_paged_attn_args* a, const DeviceInfo& dev,
   trace_pre(kKPagedJoin, st);
   const int split = p.BQ > kPagedSplitJoin ? 0 : p.BQ > kPagedHalfJoin ? 1 : 2;
   e = launch_ex(split == 2 ? paged_attn_join_kernel<2> : split == 1 ? paged_attn_join_kernel<1> : paged_attn_join_kernel<0>,
-                split ? dim3(64 * split, static_cast<unsigned>(std::min(p.BQ, ctas - 1))) : dim3(16, static_cast<unsigned>(ctas - 1)),
+                dim3(split ? 64 * split : 16, static_cast<unsigned>(std::min(p.BQ, ctas - 1))),
                 dim3(kPagedJoinThreads), 0, st, 0, p, ctas);
   trace_post(st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;

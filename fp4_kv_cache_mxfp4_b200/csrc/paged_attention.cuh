@@ -33,8 +33,8 @@
 // tile is filled in slabs of 128 dims instead: MMA 2 releases slab t when its
 // output rows t are done, and the next tile's slab t is expanded while MMA 2
 // runs on the others.  Measured, a tile takes some 6000 cycles: MMA 2 2250,
-// MMA 1 2450, softmax 1300.  Four sequences of 131,072 entries take 110 us (42 at
-// the bf16 rate), one of 1,048,576 203 us (84), both with the join.
+// MMA 1 2450, softmax 1300.  Four sequences of 131,072 entries take 109 us (42 at
+// the bf16 rate), one of 1,048,576 201 us (84), both with the join.
 // Tried and slower: a second issuing warp for MMA 1 (its MMAs and MMA 2's
 // then took 100 cycles each, 10 % in all), whole or half slabs expanded
 // before the wait for their place (7 and 4 %), one lane or one warp polling
@@ -49,7 +49,7 @@
 //   warps 12-27  softmax: S^T from tensor memory, weights to P^T, and the
 //                epilogue; warp w has keys 32 (w % 4).. and heads 16 (w / 4 - 3)..
 // Every role about fits in the 72 registers that 28 warps leave each thread
-// (24 bytes are spilled; none with 80 for a loader, 2 % slower): with the whole
+// (40 bytes are spilled; what of that lies in the loops costs: 58 bytes cost 11 %): with the whole
 // shared memory taken, L1 is too small for spilled values to stay, and each
 // reload then costs an L2 round trip.
 //
@@ -636,35 +636,35 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           cp_async_wait<0>();
           publish(t0 + 2);
         } else {
-          // window rows, in the pool's channel order, two keys of a thread at a time
+          // window rows, in the pool's channel order, four keys of a thread at
+          // a time, the first four read before the wait for the slab (in the registers of
+          // the FP4 bytes, which are then known to be dead: others cost spills)
           const bool fp8 = kind == kPagedFp8;
 #pragma unroll 1
           for (int t = t0; t < 4; t += 2) {
-            paged_wait(freed + 8 * t, ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll 1
-            for (int i = 0; i < 8; i += 2) {
-              const uint8_t* row[2];
-              uint4 x[2][2];
+            for (int i = 0; i < 8; i += 4) {
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                row[k] = lds_ptr(row_s + 8 * (stage * 128 + key0 + 4 * (i + k) + (lane >> 3)));
-                x[k][0] = x[k][1] = make_uint4(0, 0, 0, 0);
-                if (row[k]) {
-                  const uint4* src = reinterpret_cast<const uint4*>(row[k] + (fp8 ? 128 : 256) * t) + (lane & 7);
-                  x[k][0] = __ldg(src);
-                  if (!fp8) x[k][1] = __ldg(src + 8);
+              for (int k = 0; k < 4; ++k) {
+                const uint8_t* row = lds_ptr(row_s + 8 * (stage * 128 + key0 + 4 * (i + k) + (lane >> 3)));
+                raw[0][k] = raw[1][k] = make_uint4(0, 0, 0, 0);
+                if (row) {
+                  const uint4* src = reinterpret_cast<const uint4*>(row + (fp8 ? 128 : 256) * t) + (lane & 7);
+                  raw[0][k] = __ldg(src);
+                  if (!fp8) raw[1][k] = __ldg(src + 8);
                 }
               }
+              if (i == 0) paged_wait(freed + 8 * t, ph, kErrWaitSmemEmpty, abort_flag);
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
+              for (int k = 0; k < 4; ++k) {
                 const int r = key0 + 4 * (i + k) + (lane >> 3);
-                uint4 lo = x[k][0], hi = x[k][1];
+                uint4 lo = raw[0][k], hi = raw[1][k];
                 uint32_t at = 2 * t * 16384 + sw128_off(r, lane & 7), at2 = at + 16384;
                 if (fp8) {
-                  e4m3x4_to_bf16(x[k][0].x, lo.x, lo.y);
-                  e4m3x4_to_bf16(x[k][0].y, lo.z, lo.w);
-                  e4m3x4_to_bf16(x[k][0].z, hi.x, hi.y);
-                  e4m3x4_to_bf16(x[k][0].w, hi.z, hi.w);
+                  e4m3x4_to_bf16(raw[0][k].x, lo.x, lo.y);
+                  e4m3x4_to_bf16(raw[0][k].y, lo.z, lo.w);
+                  e4m3x4_to_bf16(raw[0][k].z, hi.x, hi.y);
+                  e4m3x4_to_bf16(raw[0][k].w, hi.z, hi.w);
                   const uint32_t chunk = (2 * t + ((lane >> 2) & 1)) * 16384;
                   at = chunk + sw128_off(r, 2 * (lane & 3));
                   at2 = chunk + sw128_off(r, 2 * (lane & 3) + 1);
@@ -886,20 +886,20 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 // 2(c-1)+1, 2c, 2(c+1), ...; cut[c] names it and counts them.  Partials are
 // added in a fixed order whatever the timing.
 //
-// SPLIT = 0 (many queries, few partials each): CTA (x, y) takes boundary
-// y + 1, if a query is first cut there, and its four groups of 128 threads one
-// head each.  SPLIT = 1 (fewer queries): CTA (h, y) takes head h of the y-th
-// cut query, its four groups every fourth partial each.  SPLIT = 2 (one query
-// or two): CTA (x, y) takes half of head x / 2's dims, its eight groups of 64
-// threads every eighth partial each.  A thread owns 4 dims and keeps kFlight
+// CTAs (., y) take the y-th cut query, or, where there are as many queries as
+// boundaries, boundary y + 1 if a query is first cut there.  SPLIT = 0 (many
+// queries, few partials each): a CTA's four groups of 128 threads take one
+// head each.  SPLIT = 1 (fewer queries): a CTA takes one head, its four groups
+// every fourth partial each.  SPLIT = 2 (one query or two): a CTA takes half
+// of a head's dims, its eight groups of 64 threads every eighth partial each.  A thread owns 4 dims and keeps kFlight
 // 16-byte loads in flight, the first of them over the reading of maxima and
 // sums: the chain of dependent reads bounds the kernel, not the bytes.
 //
 // Where the rule lies, attention and join of 262,144 entries in all (us):
 //   queries      1     2     4     8    12    16    20
-//   SPLIT 2   69.7  68.2  69.7  76.5  84.7  90.8  97.1
-//   SPLIT 1   72.4  69.1  66.8  69.9  76.2  79.1  82.7
-//   SPLIT 0  117.6  91.4  79.6  73.9  75.6  75.3  75.3
+//   SPLIT 2   68.2  65.9  67.6  74.5  83.2  89.0  95.3
+//   SPLIT 1   71.2  66.8  64.7  67.8  74.5  77.0  80.4
+//   SPLIT 0  118.1  91.6  77.3  71.7  73.0  71.3  71.4
 constexpr int kPagedJoinThreads = 512;
 constexpr int kPagedHalfJoin = 2, kPagedSplitJoin = 10;            // queries up to which SPLIT is 2, 1
 template <int SPLIT>
@@ -914,10 +914,10 @@ paged_attn_join_kernel(PagedAttnParams p, int ctas) {
   const int h = SPLIT ? blockIdx.x / SPLIT : 4 * blockIdx.x + g;
   const int d = SPLIT == 2 ? 4 * (t + kGroup * (blockIdx.x & 1)) : 4 * t;     // first of the thread's dims
   pdl_launch_dependents();
-  if (SPLIT && tid == 0) c0_s = 0;
+  if (tid == 0) c0_s = 0;
   pdl_wait();
   int c0 = blockIdx.y + 1;
-  if (SPLIT) {
+  if (static_cast<int>(gridDim.y) < ctas - 1) {          // fewer queries than boundaries
     const bool begins = tid + 1 < ctas && __ldcg(&p.cut[tid + 1].y) > 0;
     const uint32_t vote = __ballot_sync(0xffffffffu, begins);
     if (lane == 0) count_s[warp] = __popc(vote);
