@@ -522,3 +522,41 @@ def test_a_served_batch_step_by_step():
             if lens[b] <= K:
                 # both results against one value: twice the bar's share that their roundings take
                 np.testing.assert_allclose(po[b, 0].float().cpu().numpy(), so[0, b].float().cpu().numpy(), atol=2e-2, rtol=2e-2)
+
+
+@pytest.mark.parametrize("B,extra", [(1024, 0), (1024, 1), (5000, 3)])
+def test_block_tables_one_row_each(B, extra):
+    """The longest list of one launch, the shortest of two, and more requests than starts held in shared memory."""
+    rng = np.random.default_rng(B + extra)
+    lens, _, free, table, _ = _case(rng, B, 16, 60, 1, 0)
+    new = np.ones(B, dtype=np.int64)
+    free = np.concatenate([free, np.arange(B) + 10 ** 6])
+    s = Step(lens, new, free, table, 16, B + extra)
+    s.run()
+    _compare(s, paged.block_tables(lens, new, free, table, 16, B + extra))
+
+
+@pytest.mark.parametrize("block,width", [(1 << 30, 1), (1 << 29, 2), ((1 << 29) - 3, 2), (1, 8), (1000003, 1073)])
+def test_block_tables_at_the_largest_tables(block, width):
+    """Divisions by the block size up to the last position that a table can name."""
+    cap = block * width
+    lens = np.array([cap - 4, cap - 1, 0, block - 1 if block > 1 else 3, cap - 2, cap])
+    new = np.array([4, 2, 3, 3, 2, 0])
+    table = np.full((6, width), -1)
+    rng = np.random.default_rng(width)
+    for b in range(6):
+        have = -(-int(lens[b]) // block)
+        table[b, :have] = rng.integers(0, 1000, have)
+    s = Step(lens, new, np.arange(50) + 2000, table, block, 20)
+    s.run()
+    _compare(s, paged.block_tables(lens, new, np.arange(50) + 2000, table, block, 20))
+
+
+@pytest.mark.parametrize("B", [2, 3, 10, 11, 40])
+def test_partials_joined_for_few_and_many_queries(B):
+    """Every way that the join splits its work, with queries of no key and of one tile between long ones."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1500, 6000 if B < 12 else 2500, B)
+    lens[1::4] = rng.integers(0, 2, lens[1::4].size) * 100
+    c = Case(lens.tolist(), 1, 64, 0 if B % 2 else 40, seed=B + 50).run()
+    c.check([(b, 0) for b in range(0, B, max(1, B // 8))] + [(1, 0), (B - 1, 0)])
