@@ -24,11 +24,12 @@
 // (M = 128 dims x 4, N = 64, K = 128 keys) with the same bf16 key tile read
 // along its other axis.
 //
-// What bounds it: the data path of shared memory and L1, 128 B per cycle.  A
-// tile's 64 MMAs read 6 KB of operands each, 48 cycles (measured; the MMA rate
-// alone would allow 32), 3072 per tile; expanded keys are written at 1024, raw
-// ones pass at some 550.  One key tile (128 KB), Q (64 KB) and P^T (16 KB)
-// fill the shared memory, so there is no second tile to work on while the
+// What bounds it: the data path of shared memory and L1.  A tile's 64 MMAs
+// read 6 KB of operands each at 128 B per cycle, 48 cycles (measured; the MMA
+// rate alone would allow 32), 3072 per tile; beside them the expanded keys are
+// written (1024 cycles) and raw keys, weights and addresses pass, 3100
+// load/store wavefronts per tile in all (counted).  One key tile (128 KB), Q
+// (64 KB) and P^T (16 KB) fill the shared memory, so there is no second tile to work on while the
 // softmax runs (some 1300 cycles, 512 of them the exponentials' rate); the
 // tile is filled in slabs of 128 dims instead: MMA 2 releases slab t when its
 // output rows t are done, and the next tile's slab t is expanded while MMA 2
