@@ -26,7 +26,7 @@
 //
 // What bounds it: the data path of shared memory and L1.  A tile's 64 MMAs
 // read 6 KB of operands each at 128 B per cycle, 48 cycles (measured; the MMA
-// rate alone would allow 32), 3072 per tile; beside them the expanded keys are
+// rate alone would allow 32), half of a tile; beside them the expanded keys are
 // written (1024 cycles) and raw keys, weights and addresses pass, 3100
 // load/store wavefronts per tile in all (counted).  One key tile (128 KB), Q
 // (64 KB) and P^T (16 KB) fill the shared memory, so there is no second tile to work on while the
