@@ -448,6 +448,8 @@ def paged_attn_args(q, kv, block_table, n_vis, out, lse=None, swa=None, W=0, swa
     _need(q, "q", torch.bfloat16, None, None, 64, 512)
     _need(out, "out", torch.bfloat16, B, Q, 64, 512)
     _need(n_vis, "n_vis", torch.int32, B, Q)
+    if out.data_ptr() == q.data_ptr():
+        raise ValueError("out must not be q: several CTAs read a query while others already write")
     if lse is not None:
         _need(lse, "lse", torch.float32, B, Q, 64)
     fp4 = kv.dtype == torch.uint8

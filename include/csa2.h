@@ -588,7 +588,9 @@ csa2_status csa2_paged_rows(const csa2_paged_rows_args* a, void* stream);
  * Entries in a block that the table does not name (an id outside
  * [0, n_blocks)) are no keys; rows of the pool that no visible entry lies in
  * are not read, whatever they hold.  A query with no key gets out = 0 and
- * lse = -inf.
+ * lse = -inf.  A block may stand in several rows of the table (a shared
+ * prefix).  out and lse must not overlap any input: several CTAs read a
+ * query while others already write.
  *
  * kv_format CSA2_FMT_NVFP4: pool rows are 288-byte FP4 entries
  * (csa2_quantize_kv_fp4); CSA2_FMT_BF16: 512 bf16 values.  Blocks lie

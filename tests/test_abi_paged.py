@@ -172,3 +172,12 @@ def test_binding_checks():
                 (z(2), z(2), z(5), table, z(9, torch.int64), z(3), z(2), z(1))):
         with pytest.raises(ValueError):
             csa2.block_table_args(*bad, block_size=4)
+
+
+def test_output_over_the_queries_is_refused():
+    q = torch.zeros(2, 1, 64, 512, dtype=torch.bfloat16)
+    kv, table = torch.zeros(6, 4, 288, dtype=torch.uint8), torch.zeros(2, 3, dtype=torch.int32)
+    vis = torch.zeros(2, 1, dtype=torch.int32)
+    csa2.paged_attn_args(q, kv, table, vis, torch.zeros_like(q))
+    with pytest.raises(ValueError, match="out must not be q"):
+        csa2.paged_attn_args(q, kv, table, vis, q)

@@ -560,3 +560,12 @@ def test_partials_joined_for_few_and_many_queries(B):
     lens[1::4] = rng.integers(0, 2, lens[1::4].size) * 100
     c = Case(lens.tolist(), 1, 64, 0 if B % 2 else 40, seed=B + 50).run()
     c.check([(b, 0) for b in range(0, B, max(1, B // 8))] + [(1, 0), (B - 1, 0)])
+
+
+def test_blocks_shared_by_several_requests():
+    """A common prefix: the same blocks in several rows of the table."""
+    c = Case([600, 600, 600, 90], 1, 64, 40, seed=61)
+    for b in (1, 2):
+        c.table[b, :7], c.keys[b] = c.table[0, :7], np.concatenate([c.keys[0][:7 * 64], c.keys[b][7 * 64:]])
+    c.table_d.copy_(_i32(c.table))
+    c.run().check()
