@@ -504,10 +504,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             const uint8_t* row = nullptr;
             if (window) {
               const int64_t r = static_cast<int64_t>(b) * p.swa_rows + static_cast<int64_t>(c.row - b * p.Q) * p.swa_step + key;
-              if (key < p.W) {
-                row = p.swa + r * bytes;
-                if (p.swa_fp8) sts(wsc_s + 4 * (stage * 128 + lane + 32 * i), p.swa_scale[r]);
-              }
+              if (key < p.W) row = p.swa + r * bytes;
+              // (of absent keys too: their weight of 0 is multiplied by it)
+              if (p.swa_fp8) sts(wsc_s + 4 * (stage * 128 + lane + 32 * i), row ? p.swa_scale[r] : 0.0f);
             } else if (key < c.keys) {
               row = paged_row(p, p.table + b * p.ld_table, static_cast<uint32_t>(key), bytes);
             }
