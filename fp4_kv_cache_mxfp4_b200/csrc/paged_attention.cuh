@@ -44,7 +44,7 @@
 //                it lost hundreds of cycles per tile to the loaders)
 //   warp 1       row addresses of the tiles to come (block table, window),
 //                up to three tiles ahead, and their prefetch to L2
-//   warps 2-3    Q (TMA, then the channel order below)
+//   warps 2-3    Q (TMA, then the channel order below; warp 2 alone in bf16 pools)
 //   warps 4-11   loaders: rows -> bf16 slabs (FP4 entries of the next tile
 //                wait in registers; bf16 rows go by cp.async)
 //   warps 12-27  softmax: S^T from tensor memory, weights to P^T, and the
@@ -519,8 +519,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           if (!paged_next(p, c)) break;
           if (++stage == kPagedStages) { stage = 0; ph ^= 1; }
         }
-      } else {
+      } else if (!KVB || warp == kPagedQWarp0) {
         // ---------------------------------------------------------- Q
+        // (bf16 pools: the copy alone, one warp.  A warp whose work no one waits
+        // for could fall a phase behind on q_free.)
         const int qtid = tid - 32 * kPagedQWarp0;
         for (uint32_t part = 0;; ++part) {
           paged_wait(q_free, (part & 1) ^ 1, kErrWaitOperand, abort_flag);
