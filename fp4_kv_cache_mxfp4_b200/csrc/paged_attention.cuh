@@ -298,7 +298,7 @@ __device__ __forceinline__ void paged_mma(uint32_t tmem_d, uint32_t a_lo, uint32
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
       :: "r"(tmem_d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate) : "memory");
 }
-// One lane of a converged warp, always the same one.
+// True in one lane of a converged warp; which one is the hardware's choice.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   __syncwarp();
@@ -425,7 +425,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         // The whole warp walks along and one elected lane issues: the
         // descriptors then live in uniform registers, and an MMA costs a few
         // issue slots among busy warps.
-        const bool issuer = elect_one() && lane == 0;
+        const bool issuer = elect_one();
         uint32_t ph_q = 0;
         bool first = true;
         // descriptors of the tiles' first bytes; an offset adds to the 16-byte address field
