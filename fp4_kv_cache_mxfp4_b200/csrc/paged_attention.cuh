@@ -274,6 +274,25 @@ __device__ __forceinline__ const uint8_t* lds_ptr(uint32_t a) {
   asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
+// Wait for the end of a query's part, which may be millions of tiles: it
+// gives up only when, for as many polls, no tile's addresses were written either.
+__device__ __forceinline__ bool paged_wait_part(uint32_t bar, uint32_t parity, uint32_t progress, int err, volatile int* abort) {
+  int seen = -1;
+  while (true) {
+#pragma unroll 1
+    for (uint32_t n = 0; n < kPagedPolls && !*abort; ++n)
+      if (__all_sync(0xffffffffu, paged_try_wait(bar, parity))) return true;
+    const int now = __shfl_sync(0xffffffffu, lds_i(progress), 0);
+    if (now == seen || __any_sync(0xffffffffu, *abort)) break;
+    seen = now;
+  }
+  if (!*abort) {
+    record_error(err);
+    *abort = 1;
+  }
+  __syncwarp();
+  return false;
+}
 // (volatile: stays before the barrier that it is meant to hide)
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -384,6 +403,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t rows_free = misc32 + 136;              // [3] ... and read (16 softmax warps)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 164);
+  const uint32_t tiles_s = misc32 + 168;                              // int: tiles whose addresses were written
   const uint32_t kind_s = misc32 + 176;                               // int [3]
   float* red_s = reinterpret_cast<float*>(misc + 256);                // [4 quarters][64 heads]
   const uint32_t nref_s = misc32 + 1280;                              // float [64] minus the reference; +inf before any key
@@ -399,6 +419,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
     for (int i = 0; i < 20; ++i)
       mbar_init(bars + i, i < 4 ? kPagedLoaders / 2 : i == 8 ? (KVB ? 1 : kPagedQWarps) : i == 10 || i >= 17 ? kPagedSoftmax : 1);
     *abort_flag = 0;
+    sts(tiles_s, 0);
     fence_barrier_init();
     tma_prefetch_desc(&tmap_q);
   }
@@ -490,7 +511,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         tmem_dealloc(lds_i(misc32 + 160), 512);
       } else if (warp == 1) {
         // ---------------------------------------------------------- row addresses, 4 keys per lane
-        int stage = 0;
+        int stage = 0, tiles = 0;
         uint32_t ph = 1;
         while (true) {
           paged_wait(rows_free + 8 * stage, ph, kErrWaitSmemEmpty, abort_flag);
@@ -514,7 +535,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             if (row)
               for (int o = 0; o < bytes; o += 128) prefetch_l2(row + o);
           }
-          if (lane == 0) sts(kind_s + 4 * stage, window ? (p.swa_fp8 ? kPagedFp8 : kPagedBf16) : kPagedPool);
+          if (lane == 0) {
+            sts(kind_s + 4 * stage, window ? (p.swa_fp8 ? kPagedFp8 : kPagedBf16) : kPagedPool);
+            sts(tiles_s, ++tiles);
+          }
           paged_arrive(rows_full + 8 * stage);
           if (!paged_next(p, c)) break;
           if (++stage == kPagedStages) { stage = 0; ph ^= 1; }
@@ -525,7 +549,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         // for could fall a phase behind on q_free.)
         const int qtid = tid - 32 * kPagedQWarp0;
         for (uint32_t part = 0;; ++part) {
-          paged_wait(q_free, (part & 1) ^ 1, kErrWaitOperand, abort_flag);
+          paged_wait_part(q_free, (part & 1) ^ 1, tiles_s, kErrWaitOperand, abort_flag);
           if (qtid == 0) {
             uint64_t* arrived = reinterpret_cast<uint64_t*>(misc + (KVB ? 64 : 96));   // q_full or q_tma
             mbar_arrive_expect_tx(arrived, kTcQTileBytes);
