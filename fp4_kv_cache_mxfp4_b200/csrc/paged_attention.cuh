@@ -88,6 +88,14 @@ constexpr uint32_t kPagedPolls = 1u << 24;            // of a wait, before it gi
 constexpr int kPagedEndBar = 5;                         // named barriers: 1-4 the softmax quarters, 5 the end
 constexpr float kPagedFp4Up = 256.0f, kPagedFp4Down = 0.00390625f;
 constexpr int kPagedKeys = 128;                        // keys per tile (MMA M)
+// Tiles summed in tensor memory.  The tensor core drops what of a product lies
+// below the last bit of its accumulator, and the loss grows with the keys
+// that one accumulator takes: with keys of one sign, 5e-4 of the output after
+// 131,072 keys, 6e-3 after 1,048,576, half after 2^27.  So a longer part is summed in
+// runs of so many tiles (2e-4 at any length, measured; the bf16 weights are
+// off by up to 2^-8 each), merged in float32 in the CTA's own partial slot.
+// 148 requests of 1,048,576 entries take 25.1 ms with and without.
+constexpr int kPagedRun = 256;
 constexpr int kPagedMaxCtas = 148;                     // one per SM of a B200
 constexpr uint32_t kPagedSmem = kTcAttnSmem;
 
@@ -151,18 +159,27 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int6
   return *range_s;
 }
 
-// Walks the tiles of a CTA's range: tiles [t, t1) of query `row`, then the next query's.
+// Walks the tiles of a CTA's range: runs [t, t1) of query `row`'s tiles, then the next query's.
 struct PagedCursor {
   uint32_t left;             // tiles of the range from tile t on (below 2^32 / 148 queries' worth each)
-  int t, t1, tiles;          // this tile, the end of the range's part of the query, the query's tiles
+  int t, t1;                 // this tile, the end of its run
   int row, keys, kv_tiles;
 };
+// The query's tiles.
+__device__ __forceinline__ int paged_all(const PagedAttnParams& p, const PagedCursor& c) { return max(c.kv_tiles + p.w_tiles, 1); }
+__device__ __forceinline__ void paged_run(const PagedAttnParams& p, PagedCursor& c) {
+  c.t1 = min(paged_all(p, c), c.t + static_cast<int>(min(c.left, static_cast<uint32_t>(kPagedRun))));
+}
+// At a run's last tile: is it the last of the range's part of the query?
+__device__ __forceinline__ bool paged_part_ends(const PagedAttnParams& p, const PagedCursor& c) {
+  return c.left == 1 || c.t1 == paged_all(p, c);
+}
 __device__ __forceinline__ void paged_enter(const PagedAttnParams& p, PagedCursor& c, int row, int offset) {
   c.row = row;
-  c.tiles = paged_tiles(p, row, &c.keys);
+  paged_tiles(p, row, &c.keys);
   c.kv_tiles = (c.keys + kPagedKeys - 1) / kPagedKeys;
   c.t = offset;
-  c.t1 = static_cast<int>(min(static_cast<int64_t>(c.tiles), static_cast<int64_t>(offset) + c.left));
+  paged_run(p, c);
 }
 // The cursor at the range's first tile.
 __device__ __forceinline__ PagedCursor paged_begin(const PagedAttnParams& p, const volatile PagedRange* r) {
@@ -174,7 +191,10 @@ __device__ __forceinline__ PagedCursor paged_begin(const PagedAttnParams& p, con
 // To the next tile; false behind the last.
 __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedCursor& c) {
   if (--c.left == 0) return false;
-  if (++c.t == c.t1) paged_enter(p, c, c.row + 1, 0);
+  if (++c.t == c.t1) {
+    if (c.t == paged_all(p, c)) paged_enter(p, c, c.row + 1, 0);
+    else paged_run(p, c);
+  }
   return true;
 }
 
@@ -305,6 +325,13 @@ __device__ __forceinline__ void paged_ld_wait(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) :: "memory");
 }
+__device__ __forceinline__ void tmem_ld_32x32b_x4(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(taddr) : "memory");
+}
+__device__ __forceinline__ void paged_ld_wait(uint32_t (&r)[4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]) :: "memory");
+}
 // umma_bf16 with the descriptors' high words apart: only the low ones (the
 // addresses) change from one MMA to the next.
 __device__ __forceinline__ void paged_mma(uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
@@ -396,7 +423,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t q_full = misc32 + 64;
   const uint32_t s_full = misc32 + 72;                  // MMA 1 done (and every MMA before it)
   const uint32_t p_full = misc32 + 80;                  // P^T written, O^T rescaled (16 softmax warps)
-  const uint32_t o_full = misc32 + 88;                  // the query part's last MMA 2 done
+  const uint32_t o_full = misc32 + 88;                  // the run's last MMA 2 done
   const uint32_t q_tma = misc32 + 96;                   // Q arrived, in natural order (FP4 pools)
   const uint32_t q_free = misc32 + 104;                 // the query part's last MMA 1 done
   const uint32_t rows_full = misc32 + 112;              // [3] row addresses written
@@ -412,6 +439,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   PagedRange* range_s = reinterpret_cast<PagedRange*>(misc + 2064);
   const uint32_t row_s = misc32 + 2304;                               // [3][128] row address, null: no such key
   const uint32_t wsc_s = misc32 + 5376;                               // float [3][128] FP8 row scales
+  const uint32_t ref0_s = misc32 + 6912;                              // float [64] reference of the part's earlier runs
+  const uint32_t sum0_s = misc32 + 7168;                              // float [64] ... their sum
+  const uint32_t fac0_s = misc32 + 7424;                              // float [64] ... and their factor in the merge
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 32) {
@@ -448,7 +478,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         // issue slots among busy warps.
         const bool issuer = elect_one();
         uint32_t ph_q = 0;
-        bool first = true;
+        bool first = true, fresh = true;                // of a run, of a query's part
         // descriptors of the tiles' first bytes; an offset adds to the 16-byte address field
         const uint64_t kd = umma_desc_sw128_kmajor(kt), qd = umma_desc_sw128_kmajor(qt);
         const uint64_t vd = umma_desc_sw128_mnmajor(kt, 16384), pd = umma_desc_sw128_mnmajor(pt, 16384);
@@ -457,10 +487,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         // The walk to the next tile is done while the softmax runs: between MMA 2
         // and the next MMA 1 every instruction costs (28 warps share the
         // instruction cache).
-        bool last = c.t + 1 == c.t1;
+        bool last = c.t + 1 == c.t1, ends = last && paged_part_ends(p, c);
         for (uint32_t ph = 0;; ph ^= 1) {
           bool ok = true;
-          if (first) {
+          if (fresh) {
             ok = paged_wait(q_full, ph_q, kErrWaitOperand, abort_flag);
             ph_q ^= 1;
           }
@@ -481,10 +511,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           }
           if (issuer) {
             paged_commit(s_full);
-            if (last) paged_commit(q_free);
+            if (ends) paged_commit(q_free);
           }
           __syncwarp();
-          const bool more = paged_next(p, c), next_last = c.t + 1 == c.t1;
+          const bool more = paged_next(p, c), next_last = c.t + 1 == c.t1, next_ends = next_last && paged_part_ends(p, c);
           ok = paged_wait(p_full, ph, kErrWaitOperand, abort_flag) && ok;
           tc_fence_after();
           da = static_cast<uint32_t>(vd);
@@ -504,7 +534,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           __syncwarp();
           if (!more) break;
           first = last;
+          fresh = ends;
           last = next_last;
+          ends = next_ends;
         }
         paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
         tc_fence_after();
@@ -574,7 +606,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             fence_async_smem();
             paged_arrive(q_full);
           }
-          c.left -= c.t1 - c.t;
+          c.left -= min(c.left, static_cast<uint32_t>(paged_all(p, c) - c.t));
           if (c.left == 0) break;
           paged_enter(p, c, c.row + 1, 0);
         }
@@ -716,10 +748,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
       uint32_t ph_o = 0;
       int stage = 0;
       float sum[16];                                    // this key's weights, summed over the tiles, per head
-      bool first = true, part_begins = false;
+      bool first = true, merge = false, part_begins = false;     // merge: the part has earlier runs
       for (uint32_t it = 0;; ++it) {
         if (first) {
-          part_begins = c.t == 0;
+          if (!merge) part_begins = c.t == 0;
           if (quarter == 0 && lane < 16) sts(nref_s + 4 * (head0 + lane), INFINITY);
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
@@ -829,9 +861,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         first = false;
 
         if (c.t + 1 == c.t1) {
-          // -------------------------------------- the query's part is complete
+          // -------------------------------------- the run is complete
           const int row = c.row;
-          const bool whole = part_begins && c.t1 == c.tiles;
+          const bool ends = paged_part_ends(p, c), whole = part_begins && c.t1 == paged_all(p, c);
           const int slot = 2 * blockIdx.x + (part_begins ? 1 : 0);
           {
             const float l = warp_reduce_heads16<false>(sum, lane);
@@ -840,14 +872,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           paged_bar(bar, 128);
           if (quarter == 0) {
             const int h = head0 + (lane & 15);
-            const float l = (red_s[h] + red_s[64 + h]) + (red_s[128 + h] + red_s[192 + h]);
-            const float ref = -lds_f(nref_s + 4 * h), up = KVB ? 1.0f : kPagedFp4Up;
-            const float f = whole ? (l > 0.0f ? up / l : 0.0f) : up;
+            float l = (red_s[h] + red_s[64 + h]) + (red_s[128 + h] + red_s[192 + h]);
+            float ref = -lds_f(nref_s + 4 * h), f = KVB ? 1.0f : kPagedFp4Up, f0 = 0.0f;
+            if (merge) {
+              const float ref0 = lds_f(ref0_s + 4 * h), top = fmaxf(ref0, ref);
+              f0 = ref0 == top ? 1.0f : ex2(ref0 - top);
+              const float f1 = ref == top ? 1.0f : ex2(ref - top);
+              l = lds_f(sum0_s + 4 * h) * f0 + l * f1;
+              f *= f1;
+              ref = top;
+            }
+            if (whole) {
+              const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+              f *= inv;
+              f0 *= inv;
+            }
             const float v = l > 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
             __syncwarp();
             if (lane < 16) {
               sts(fac_s + 4 * h, f);
-              if (!*abort_flag) {
+              sts(fac0_s + 4 * h, f0);
+              sts(ref0_s + 4 * h, ref);
+              sts(sum0_s + 4 * h, l);
+              if (ends && !*abort_flag) {
                 if (!whole) {
                   *reinterpret_cast<float2*>(p.ml + (slot * 64 + h) * 2) = make_float2(ref, l);
                 } else if (p.lse) {
@@ -865,36 +912,64 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           const int ch = KVB ? lane : (lane & ~7) + paged_channel(lane & 7);
           constexpr int kPair = KVB ? 1 : 2;
           const int odd = ch & 1;
-          float fac[16];
+          // lanes pair up: the even one writes dims d, d + 1 of head j, the odd one of head j + 1
+          auto put = [&](int d, int j, float a, float b) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, kPair);
+            const uint32_t v = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
+            if (store)
+              *reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(row) * 64 + head0 + odd + j) * 512 + (d & ~1)) = v;
+          };
+          float* part = p.opart + (static_cast<int64_t>(slot) * 64 + head0) * 512 + 32 * quarter + ch;
+          if (!merge) {
+            float fac[16];
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 f = lds_f4(fac_s + 4 * (head0 + j));
-            fac[j] = f.x; fac[j + 1] = f.y; fac[j + 2] = f.z; fac[j + 3] = f.w;
-          }
+            for (int j = 0; j < 16; j += 4) {
+              const float4 f = lds_f4(fac_s + 4 * (head0 + j));
+              fac[j] = f.x; fac[j + 1] = f.y; fac[j + 2] = f.z; fac[j + 3] = f.w;
+            }
 #pragma unroll 1
-          for (int t = 0; t < 4; ++t) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(tmem + lanes + 64 + 64 * t + head0, r);
-            paged_ld_wait(r);
-            const int d = 128 * t + 32 * quarter + ch;
-            if (whole) {
-              // lanes pair up: the even one writes dims d, d + 1 of head j, the odd one of head j + 1
-              __nv_bfloat16* op = p.out + (static_cast<int64_t>(row) * 64 + head0 + odd) * 512 + (d & ~1);
+            for (int t = 0; t < 4; ++t) {
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(tmem + lanes + 64 + 64 * t + head0, r);
+              paged_ld_wait(r);
+              if (whole) {
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                const float a = __uint_as_float(r[j]) * fac[j], b = __uint_as_float(r[j + 1]) * fac[j + 1];
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, kPair);
-                const uint32_t v = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-                if (store) *reinterpret_cast<uint32_t*>(op + j * 512) = v;
+                for (int j = 0; j < 16; j += 2)
+                  put(128 * t + 32 * quarter + ch, j, __uint_as_float(r[j]) * fac[j], __uint_as_float(r[j + 1]) * fac[j + 1]);
+              } else if (store) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[j * 512 + 128 * t] = __uint_as_float(r[j]) * fac[j];
               }
-            } else if (store) {
-              float* op = p.opart + (static_cast<int64_t>(slot) * 64 + head0) * 512 + d;
+            }
+          } else {
+            // each thread adds to what it wrote itself (rolled: seldom run, and few registers)
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+              const int t = i >> 2, j = 4 * (i & 3);
+              uint32_t r[4];
+              float o[4];
+              float* at = part + j * 512 + 128 * t;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) op[j * 512] = __uint_as_float(r[j]) * fac[j];
+              for (int k = 0; k < 4; ++k) o[k] = at[k * 512];
+              tmem_ld_32x32b_x4(tmem + lanes + 64 + 64 * t + head0 + j, r);
+              const float4 f = lds_f4(fac_s + 4 * (head0 + j)), f0 = lds_f4(fac0_s + 4 * (head0 + j));
+              paged_ld_wait(r);
+              o[0] = fmaf(o[0], f0.x, __uint_as_float(r[0]) * f.x);
+              o[1] = fmaf(o[1], f0.y, __uint_as_float(r[1]) * f.y);
+              o[2] = fmaf(o[2], f0.z, __uint_as_float(r[2]) * f.z);
+              o[3] = fmaf(o[3], f0.w, __uint_as_float(r[3]) * f.w);
+              if (whole) {
+                put(128 * t + 32 * quarter + ch, j, o[0], o[1]);
+                put(128 * t + 32 * quarter + ch, j + 2, o[2], o[3]);
+              } else if (store) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) at[k * 512] = o[k];
+              }
             }
           }
           tc_fence_before();
           paged_bar(bar, 128);                     // nref_s and fac_s are free
+          merge = !ends;
           first = true;
         }
         if (!paged_next(p, c)) break;

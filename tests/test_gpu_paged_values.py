@@ -3,10 +3,13 @@ beside rows that are not finite.  Cases and tolerances as in test_gpu_paged."""
 
 import math
 
-import torch
+import numpy as np
 import pytest
+import torch
 
 from fp4_kv_cache_mxfp4_b200 import csa2
+from oracle import fp4
+from parity import f32
 from test_gpu_paged import Case
 
 pytestmark = pytest.mark.gpu
@@ -51,6 +54,86 @@ def test_query_parts_that_take_seconds():
     csa2.csa2_paged_attn(args, csa2.workspace(args, csa2.WS_PAGED_ATTN))
     torch.cuda.synchronize()
     assert csa2.csa2_device_status() == (0, 0)
-    assert torch.all(torch.isfinite(out)) and torch.all(out[1::2] == 0)
+    assert torch.all(out[::2] == 1) and torch.all(out[1::2] == 0)
     # float32: log2 and a product, half a unit in the last place each, log2 with one more
     assert torch.all((lse[::2] - 27 * math.log(2)).abs() <= 2.0 ** -22 * 27 * math.log(2)) and torch.all(lse[1::2] == -math.inf)
+
+
+@pytest.mark.parametrize("B", [148, 100])                # whole queries in one CTA, and cut ones
+@pytest.mark.parametrize("kv", ["fp4", "bf16"])
+def test_output_sums_of_millions_of_keys(kv, B):
+    """2^22 equal keys per request, all weights 1: the output is the key
+    itself, to the bit.  A run's sum of 2^15 keys of 8 bits needs 23, the
+    128 or more runs are added in float32, 2^-24 each: a relative 2^-16 against
+    half a step of bf16, 2^-9 at least.  (One float32 accumulator
+    over all of them keeps 24 bits of the 30 and loses a percent or more.)"""
+    block, per_row = 4096, 1024
+    if kv == "fp4":
+        pool = torch.empty(1, block, 288, dtype=torch.uint8)
+        codes = [1 + (c % 7) + 8 * (c % 2) for c in range(512)]
+        pool[..., :256] = torch.tensor([codes[2 * i] | codes[2 * i + 1] << 4 for i in range(256)])
+        pool[..., 256:] = torch.tensor([0x38 + (i % 8) for i in range(32)])            # 1 + m / 8
+        key = torch.from_numpy(fp4.dequantize_kv_fp4(pool[0, :1].numpy())[0]).float()
+    else:
+        key = (1 + (torch.arange(512) % 128) / 128) * (1 - 2 * (torch.arange(512) % 2))
+        pool = key.to(torch.bfloat16).expand(1, block, 512).contiguous()
+    table = torch.zeros(B, per_row, dtype=torch.int32, device="cuda")
+    vis = torch.full((B, 1), block * per_row, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, 1, 64, 512, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    args = csa2.paged_attn_args(q, pool.cuda(), table, vis, out)
+    csa2.csa2_paged_attn(args, csa2.workspace(args, csa2.WS_PAGED_ATTN))
+    torch.cuda.synchronize()
+    assert csa2.csa2_device_status() == (0, 0)
+    assert torch.equal(out.float().cpu(), key.expand(B, 1, 64, 512))
+
+
+@pytest.mark.parametrize("kv,q_std,scale,sizes", [
+    ("fp4", 1.0, 0.0, (1, 1, 1, 1, 1, 1)), ("fp4", 1.0, 0.0, (0.2, 1, 0.5, 2, 0.1, 1.5)),
+    ("bf16", 1.0, 0.0, (1, 0.3, 1.2, 0.6, 1, 1)), ("fp4", 4.0, 0.2, (0.5, 0.8, 1, 0.7, 0.9, 1)),
+])
+def test_runs_of_a_long_part_are_merged(kv, q_std, scale, sizes):
+    """Some 475 tiles per CTA, more than one run, whole and cut queries, with
+    maxima that grow and fall along the cache.  The pool has six blocks that
+    stand in the table again and again: the definition over each entry once,
+    with the number of its appearances as a factor of its weight."""
+    P, B = 512, 20
+    g, rng = torch.Generator().manual_seed(74), np.random.default_rng(74)
+    x = (torch.randn(6, P, 512, generator=g) * torch.tensor(sizes)[:, None, None]).to(torch.bfloat16)
+    if kv == "fp4":
+        raw = fp4.quantize_kv_fp4(f32(x).reshape(-1, 512))
+        pool, keys = torch.from_numpy(raw).view(6, P, 288), fp4.dequantize_kv_fp4(raw)
+    else:
+        pool, keys = x, f32(x).reshape(-1, 512).astype(np.float64)
+    width = 1100
+    table = np.repeat(rng.integers(0, 6, (B, width // 50)), 50, axis=1)                # the same block 50 times
+    n = rng.integers(300_000, P * width, B)
+    q = (torch.randn(B, 1, 64, 512, generator=g) * q_std).to(torch.bfloat16)
+    out, lse = torch.empty_like(q, device="cuda"), torch.empty(B, 1, 64, device="cuda")
+    args = csa2.paged_attn_args(q.cuda(), pool.cuda(), torch.tensor(table, dtype=torch.int32, device="cuda"),
+                                torch.tensor(n, dtype=torch.int32, device="cuda")[:, None], out, lse, scale=scale)
+    csa2.csa2_paged_attn(args, csa2.workspace(args, csa2.WS_PAGED_ATTN))
+    torch.cuda.synchronize()
+    assert csa2.csa2_device_status() == (0, 0)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    scale = scale or 512 ** -0.5
+    for b in range(B):
+        times = np.repeat(np.bincount(table[b, : n[b] // P], minlength=6), P).astype(np.float64)
+        if n[b] % P:
+            at = table[b, n[b] // P] * P
+            times[at: at + n[b] % P] += 1
+        qb = f32(q[b, 0]).astype(np.float64)
+        z = np.where(times > 0, qb @ keys.T * scale, -np.inf)
+        m = z.max(1, keepdims=True)
+        w = times * np.exp(z - m)
+        l = w.sum(1, keepdims=True)
+        w /= l
+        o, A = w @ keys, w @ np.abs(keys)
+        e = (512 * 2.0 ** -24 * scale * (np.abs(qb) @ np.abs(keys).T)).max(1, keepdims=True) + 2.0 ** -20
+        # bf16 of the output and of the weights, logits (as in test_gpu_paged), and a run's sum, 2^-25 per key of 2^15
+        tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2 * e + 2.0 ** -10) * A
+        err = np.abs(out[b, 0] - o)
+        assert np.all(err <= tol), f"request {b}: {np.max(err / tol):.2f} of the tolerance"
+        # the sum: a thread adds up to 256 tiles' weights, 2^-24 each
+        want = (m + np.log(l))[:, 0]
+        assert np.all(np.abs(lse[b, 0] - want) <= e[:, 0] + 2.0 ** -16 + 2.0 ** -22 * np.abs(want)), f"lse of {b}"
