@@ -887,7 +887,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               f *= inv;
               f0 *= inv;
             }
-            const float v = l > 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            const float v = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.69314718055994531f;   // (NaN stays NaN)
             __syncwarp();
             if (lane < 16) {
               sts(fac_s + 4 * h, f);
@@ -1096,7 +1096,7 @@ paged_attn_join_kernel(PagedAttnParams p, int ctas) {
   packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(row) * 64 + h) * 512 + d) = packed;
   if (p.lse && d == 0)
-    p.lse[static_cast<int64_t>(row) * 64 + h] = (L > 0.0f) ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+    p.lse[static_cast<int64_t>(row) * 64 + h] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace csa2

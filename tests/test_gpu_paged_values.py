@@ -137,3 +137,24 @@ def test_runs_of_a_long_part_are_merged(kv, q_std, scale, sizes):
         # the sum: a thread adds up to 256 tiles' weights, 2^-24 each
         want = (m + np.log(l))[:, 0]
         assert np.all(np.abs(lse[b, 0] - want) <= e[:, 0] + 2.0 ** -16 + 2.0 ** -22 * np.abs(want)), f"lse of {b}"
+
+
+@pytest.mark.parametrize("kv", ["fp4", "bf16"])
+@pytest.mark.parametrize("lens", [[300, 5, 0, 1000], [300] * 160])       # cut, and whole in one CTA
+def test_a_head_that_is_not_a_number(kv, lens):
+    """A NaN in a query's head gives NaN there, in the log-sum-exp too (-inf
+    says that there was no key), and leaves every other head as it was."""
+    c = Case(lens, 1, 64, 0, kv, seed=75).run()
+    out, lse = c.out.clone(), c.lse.clone()
+    at = [(0, 3), (1, 63), (2 if len(lens) == 4 else 7, 16)]
+    for b, h in at:
+        c.q_d[b, 0, h, 9 * b] = float("nan")
+    c.run()
+    torch.cuda.synchronize()
+    for b, h in at:
+        if lens[b]:
+            assert torch.all(torch.isnan(c.out[b, 0, h])) and torch.isnan(c.lse[b, 0, h]), (b, h)
+        else:
+            assert torch.all(c.out[b, 0, h] == 0) and torch.isneginf(c.lse[b, 0, h])
+        c.out[b, 0, h], c.lse[b, 0, h] = out[b, 0, h], lse[b, 0, h]
+    assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
