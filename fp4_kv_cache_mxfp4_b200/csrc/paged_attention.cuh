@@ -86,6 +86,10 @@ static_assert(256 * kPagedLoaderRegs + 128 * kPagedOtherRegs <= 384 * 72, "regis
 constexpr int kPagedStages = 3;                        // tiles whose row addresses are kept
 constexpr uint32_t kPagedPolls = 1u << 24;            // of a wait, before it gives up
 constexpr int kPagedEndBar = 5;                         // named barriers: 1-4 the softmax quarters, 5 the end
+// Minus the reference of a head that has none yet.  Finite: a logit of -inf
+// (finite entries may reach it in float32) then has weight 0, where -inf + inf
+// would be NaN; any other logit passes it and moves the reference.
+constexpr float kPagedNoRef = 3.0e38f;
 constexpr float kPagedFp4Up = 256.0f, kPagedFp4Down = 0.00390625f;
 constexpr int kPagedKeys = 128;                        // keys per tile (MMA M)
 // Tiles summed in tensor memory.  The tensor core drops what of a product lies
@@ -433,7 +437,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   const uint32_t tiles_s = misc32 + 168;                              // int: tiles whose addresses were written
   const uint32_t kind_s = misc32 + 176;                               // int [3]
   float* red_s = reinterpret_cast<float*>(misc + 256);                // [4 quarters][64 heads]
-  const uint32_t nref_s = misc32 + 1280;                              // float [64] minus the reference; +inf before any key
+  const uint32_t nref_s = misc32 + 1280;                              // float [64] minus the reference
   const uint32_t fac_s = misc32 + 1536;                               // float [64] rescale factor, later 1 / sum
   int64_t* warp_s = reinterpret_cast<int64_t*>(misc + 1792);          // [33]
   PagedRange* range_s = reinterpret_cast<PagedRange*>(misc + 2064);
@@ -752,7 +756,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
       for (uint32_t it = 0;; ++it) {
         if (first) {
           if (!merge) part_begins = c.t == 0;
-          if (quarter == 0 && lane < 16) sts(nref_s + 4 * (head0 + lane), INFINITY);
+          if (quarter == 0 && lane < 16) sts(nref_s + 4 * (head0 + lane), kPagedNoRef);
 #pragma unroll
           for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
           paged_bar(bar, 128);
@@ -765,8 +769,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         if (!KVB && window) rs *= kPagedFp4Down;
         paged_wait(s_full, it & 1, kErrWaitTmemFull, abort_flag);
         tc_fence_after();
-        // y = exp2(logit - reference) in log2 units; a head without a reference
-        // yet has +inf.  The weights go to P^T before the vote on whether some
+        // y = exp2(logit - reference) in log2 units.  The weights go to P^T before the vote on whether some
         // reference must move (then they are made again), and into the sums
         // after the hand-over: both off the path from S^T to MMA 2.
         float y[16];
@@ -824,7 +827,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
             const float mt = fmaxf(fmaxf(red_s[h], red_s[64 + h]), fmaxf(red_s[128 + h], red_s[192 + h]));
             const float ref = -lds_f(nref_s + 4 * h);
             const bool move = mt > ref + kTcRefSlack;
-            const float f = ex2(ref - mt), fac = (move && ref != -INFINITY) ? f : 1.0f;
+            const float f = ex2(ref - mt), fac = move ? f : 1.0f;
             __syncwarp();
             if (lane < 16) {
               sts(fac_s + 4 * h, fac);
@@ -1058,7 +1061,7 @@ paged_attn_join_kernel(PagedAttnParams p, int ctas) {
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
 #pragma unroll
   for (int j = 0; j < kMl; ++j) {
-    const float f = M == -INFINITY ? 0.0f : exp2f(v[j].x - M);
+    const float f = exp2f(v[j].x - M);
     L += f * v[j].y;
     if (t < 32 && lane + 32 * j < n) w_s[SPLIT ? 0 : g][lane + 32 * j] = f;        // (SPLIT: the groups write the same)
   }

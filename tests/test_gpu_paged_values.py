@@ -158,3 +158,24 @@ def test_a_head_that_is_not_a_number(kv, lens):
             assert torch.all(c.out[b, 0, h] == 0) and torch.isneginf(c.lse[b, 0, h])
         c.out[b, 0, h], c.lse[b, 0, h] = out[b, 0, h], lse[b, 0, h]
     assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+@pytest.mark.parametrize("lens,far", [([600], 256), ([600], 700), ([520] * 150, 256)])
+def test_logits_below_the_range_of_float32(lens, far):
+    """Finite entries whose logits are -2^195: -inf in float32, weight 0, also
+    where they fill a query's first tiles and no reference exists yet.
+    Expected: the definition over the other keys."""
+    c = Case(lens, 1, 64, 16, "bf16", seed=76)
+    c.pool[:, :, 0] = 0
+    c.swa[:, :, 0] = 0
+    c.win[..., 0] = 0
+    c.q[..., 0] = 0
+    c.q_d[..., 0] = 2.0 ** 100
+    for b, n in enumerate(lens):
+        rows = [(int(c.table[b, j // 64]), j % 64) for j in range(min(far, n))]
+        c.pool[[r[0] for r in rows], [r[1] for r in rows], 0] = -2.0 ** 100
+        c.keys[b] = c.keys[b][far:]
+        c.keys[b][:, 0] = 0
+    c.run()
+    c.vis = np.maximum(c.vis - far, 0)
+    c.check([(b, 0) for b in range(0, len(lens), 13)])
