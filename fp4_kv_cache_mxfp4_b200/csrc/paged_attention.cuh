@@ -469,8 +469,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   if (tid == 0) p.cut[blockIdx.x] = range.parts > 0 ? make_int2(range.row, range.parts) : make_int2(-1, 0);
 
   // Every role walks the same tiles.  Waits are bounded; after one gave up
-  // the others return at once, and every role still walks to its end (the
-  // named barriers stay matched), without writing results.
+  // the others return at once.  The MMA warp and the softmax warps, which share
+  // named barriers, then walk to their end, without writing results; the
+  // row addresses and the loaders stop, so that no address is followed that
+  // was not written for its tile.
   if (range.lo < range.hi) {
     if (warp < kPagedLoader0) {
       regs_down<kPagedOtherRegs>();
@@ -550,7 +552,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         int stage = 0, tiles = 0;
         uint32_t ph = 1;
         while (true) {
-          paged_wait(rows_free + 8 * stage, ph, kErrWaitSmemEmpty, abort_flag);
+          // (after any wait gave up, rows_free no longer says that the loaders are through)
+          if (!paged_wait(rows_free + 8 * stage, ph, kErrWaitSmemEmpty, abort_flag) || __any_sync(0xffffffffu, *abort_flag)) break;
           const bool window = c.t >= c.kv_tiles;
           const int b = c.row / p.Q;
           const int key0 = (window ? c.t - c.kv_tiles : c.t) * kPagedKeys + lane;
@@ -647,11 +650,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         fence_async_smem();
         paged_arrive(full + 8 * t);
       };
-      paged_wait(rows_full + 8 * 0, 0, kErrWaitOperand, abort_flag);
-      fetch(0);
       int stage = 0;
       uint32_t ph_rows = 0;
-      for (uint32_t ph = 1;; ph ^= 1) {                 // ph: MMA 2 of the tile before has released the slab
+      // Addresses are followed only if they were written.
+      bool ok = paged_wait(rows_full + 8 * 0, 0, kErrWaitOperand, abort_flag);
+      if (ok) fetch(0);
+      for (uint32_t ph = 1; ok; ph ^= 1) {              // ph: MMA 2 of the tile before has released the slab
         if (!KVB && kind == kPagedPool) {
           // (rolled: the kernel's hot code should stay in the instruction cache)
           uint32_t chunk = kt + (2 * t0 + (u >> 1)) * 16384 + sw128_off(key0 + kk, 4 * (u & 1));
@@ -740,8 +744,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         }
         if (--left == 0) break;
         if (++stage == kPagedStages) { stage = 0; ph_rows ^= 1; }
-        paged_wait(rows_full + 8 * stage, ph_rows, kErrWaitOperand, abort_flag);
-        fetch(stage);                                   // behind the tile's last fence, which would wait for the loads
+        ok = paged_wait(rows_full + 8 * stage, ph_rows, kErrWaitOperand, abort_flag);
+        if (ok) fetch(stage);                           // behind the tile's last fence, which would wait for the loads
       }
     } else {
       // ------------------------------------------------------------ softmax
