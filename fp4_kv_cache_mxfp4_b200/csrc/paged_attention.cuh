@@ -237,6 +237,12 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, int er
   __syncwarp();
   return false;
 }
+// Before a role ends: waits, with the same limit whatever gave up before, for its own copy or MMAs.
+__device__ __forceinline__ void paged_drain(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t n = 0; n < kPagedPolls; ++n)
+    if (__all_sync(0xffffffffu, paged_try_wait(bar, parity))) return;
+}
 __device__ __forceinline__ void paged_arrive(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
@@ -435,6 +441,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 164);
   const uint32_t tiles_s = misc32 + 168;                              // int: tiles whose addresses were written
+  const uint32_t all_done = misc32 + 192;               // after a wait gave up: every MMA done
   const uint32_t kind_s = misc32 + 176;                               // int [3]
   float* red_s = reinterpret_cast<float*>(misc + 256);                // [4 quarters][64 heads]
   const uint32_t nref_s = misc32 + 1280;                              // float [64] minus the reference
@@ -452,6 +459,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
     uint64_t* bars = reinterpret_cast<uint64_t*>(misc);  // in the order above
     for (int i = 0; i < 20; ++i)
       mbar_init(bars + i, i < 4 ? kPagedLoaders / 2 : i == 8 ? (KVB ? 1 : kPagedQWarps) : i == 10 || i >= 17 ? kPagedSoftmax : 1);
+    mbar_init(bars + 24, 1);                            // all_done
     *abort_flag = 0;
     sts(tiles_s, 0);
     fence_barrier_init();
@@ -545,6 +553,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           ends = next_ends;
         }
         paged_bar(kPagedEndBar, 32 * (kPagedSoftmax + 1));
+        if (__any_sync(0xffffffffu, *abort_flag)) {
+          if (issuer) paged_commit(all_done);
+          paged_drain(all_done, 0);
+        }
         tc_fence_after();
         tmem_dealloc(lds_i(misc32 + 160), 512);
       } else if (warp == 1) {
@@ -587,16 +599,18 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         // (bf16 pools: the copy alone, one warp.  A warp whose work no one waits
         // for could fall a phase behind on q_free.)
         const int qtid = tid - 32 * kPagedQWarp0;
-        for (uint32_t part = 0;; ++part) {
-          paged_wait_part(q_free, (part & 1) ^ 1, tiles_s, kErrWaitOperand, abort_flag);
+        uint32_t sent = 0;                              // copies, one per part
+        while (true) {
+          if (!paged_wait_part(q_free, (sent & 1) ^ 1, tiles_s, kErrWaitOperand, abort_flag)) break;
           if (qtid == 0) {
             uint64_t* arrived = reinterpret_cast<uint64_t*>(misc + (KVB ? 64 : 96));   // q_full or q_tma
             mbar_arrive_expect_tx(arrived, kTcQTileBytes);
             const uint64_t pol = l2_policy_evict_first();
             for (int k = 0; k < 8; ++k) tma_load_2d(smem + kTcKeyTileBytes + k * 8192, &tmap_q, arrived, 64 * k, c.row * 64, pol);
           }
+          ++sent;
           if (!KVB) {
-            paged_wait(q_tma, part & 1, kErrWaitOperand, abort_flag);
+            if (!paged_wait(q_tma, (sent & 1) ^ 1, kErrWaitOperand, abort_flag)) break;
             for (int i = qtid; i < static_cast<int>(kTcQTileBytes / 16); i += 4 * 32 * kPagedQWarps) {
               uint4 v[4];
 #pragma unroll
@@ -617,6 +631,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           if (c.left == 0) break;
           paged_enter(p, c, c.row + 1, 0);
         }
+        if (sent > 0) paged_drain(KVB ? q_full : q_tma, (sent & 1) ^ 1);
       }
     } else if (warp < kPagedSoftmax0) {
       // ------------------------------------------------------------ loaders
