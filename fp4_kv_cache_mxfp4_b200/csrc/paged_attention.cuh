@@ -478,8 +478,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 
   // Every role walks the same tiles.  Waits are bounded; after one gave up
   // the others return at once.  The MMA warp and the softmax warps, which share
-  // named barriers, then walk to their end, without writing results; the
-  // row addresses and the loaders stop, so that no address is followed that
+  // named barriers, then walk to their end and leave NaN for every query that
+  // was not finished, in partials too (the join runs all the same); the row
+  // addresses and the loaders stop, so that no address is followed that
   // was not written for its tile.
   if (range.lo < range.hi) {
     if (warp < kPagedLoader0) {
@@ -904,6 +905,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               f *= f1;
               ref = top;
             }
+            if (*abort_flag) f = l = NAN;
             if (whole) {
               const float inv = l > 0.0f ? 1.0f / l : 0.0f;
               f *= inv;
@@ -916,12 +918,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               sts(fac0_s + 4 * h, f0);
               sts(ref0_s + 4 * h, ref);
               sts(sum0_s + 4 * h, l);
-              if (ends && !*abort_flag) {
-                if (!whole) {
-                  *reinterpret_cast<float2*>(p.ml + (slot * 64 + h) * 2) = make_float2(ref, l);
-                } else if (p.lse) {
-                  p.lse[static_cast<int64_t>(row) * 64 + h] = v;
-                }
+              if (ends && !whole) {
+                *reinterpret_cast<float2*>(p.ml + (slot * 64 + h) * 2) = make_float2(ref, l);
+              } else if (ends && p.lse) {
+                p.lse[static_cast<int64_t>(row) * 64 + h] = v;
               }
             }
           }
@@ -929,7 +929,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           paged_wait(o_full, ph_o, kErrWaitTmemFull, abort_flag);
           tc_fence_after();
           ph_o ^= 1;
-          const bool store = !*abort_flag;
+          if (*abort_flag) sts(fac_s + 4 * (head0 + (lane & 15)), NAN);
+          __syncwarp();
           // the channel of this lane's dim, and the lane with the next one (its partner)
           const int ch = KVB ? lane : (lane & ~7) + paged_channel(lane & 7);
           constexpr int kPair = KVB ? 1 : 2;
@@ -938,8 +939,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
           auto put = [&](int d, int j, float a, float b) {
             const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, kPair);
             const uint32_t v = odd ? pack_bf16x2(got, b) : pack_bf16x2(a, got);
-            if (store)
-              *reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(row) * 64 + head0 + odd + j) * 512 + (d & ~1)) = v;
+            *reinterpret_cast<uint32_t*>(p.out + (static_cast<int64_t>(row) * 64 + head0 + odd + j) * 512 + (d & ~1)) = v;
           };
           float* part = p.opart + (static_cast<int64_t>(slot) * 64 + head0) * 512 + 32 * quarter + ch;
           if (!merge) {
@@ -958,7 +958,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
 #pragma unroll
                 for (int j = 0; j < 16; j += 2)
                   put(128 * t + 32 * quarter + ch, j, __uint_as_float(r[j]) * fac[j], __uint_as_float(r[j + 1]) * fac[j + 1]);
-              } else if (store) {
+              } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) part[j * 512 + 128 * t] = __uint_as_float(r[j]) * fac[j];
               }
@@ -983,7 +983,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
               if (whole) {
                 put(128 * t + 32 * quarter + ch, j, o[0], o[1]);
                 put(128 * t + 32 * quarter + ch, j + 2, o[2], o[3]);
-              } else if (store) {
+              } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) at[k * 512] = o[k];
               }

@@ -644,7 +644,9 @@ csa2_status csa2_paged_attn(const csa2_paged_attn_args* a, void* ws,
 size_t csa2_workspace_size(const void* args, int32_t which);
 
 /* Reads and clears the device-side failure word of the current device
- * (bounded waits that gave up, internal limits exceeded).  Synchronises
+ * (bounded waits that gave up, internal limits exceeded).  The outputs of a
+ * call that recorded a failure are undefined (csa2_paged_attn leaves NaN for
+ * the queries that a wait left unfinished).  Synchronises
  * `stream`.  Returns CSA2_OK when clear, CSA2_ERR_DEVICE otherwise and
  * stores the recorded code in *code (may be NULL). */
 csa2_status csa2_device_status(int32_t* code, void* stream);
