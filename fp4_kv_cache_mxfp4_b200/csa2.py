@@ -376,6 +376,23 @@ def _one_device(tensors):
     return device
 
 
+def _need_apart(out, name, **inputs):
+    """An output that shares no byte with any input.  An input's rows (its
+    first dimension, dense themselves) may lie apart, and out between them."""
+    lo = out.data_ptr()
+    hi = lo + out.numel() * out.element_size()
+    for what, t in inputs.items():
+        if t is None or t.numel() == 0:
+            continue
+        n, at, es = t.shape[0], t.data_ptr(), t.element_size()
+        size = (1 + sum((m - 1) * s for m, s in zip(t.shape[1:], t.stride()[1:]))) * es
+        step = max(t.stride(0) * es, 1) if n > 1 else size
+        i = max(0, (lo - at - size) // step + 1)           # the first row that ends behind lo
+        if i < n and at + i * step < hi:
+            raise ValueError(f"{name} must not be {what} or overlap it: several CTAs read a query's inputs while others "
+                             f"already write")
+
+
 def _launch(call, what, device, stream, *args):
     """call(*args, stream) with the tensors' device current (the library
     launches on the current device)."""
@@ -448,8 +465,6 @@ def paged_attn_args(q, kv, block_table, n_vis, out, lse=None, swa=None, W=0, swa
     _need(q, "q", torch.bfloat16, None, None, 64, 512)
     _need(out, "out", torch.bfloat16, B, Q, 64, 512)
     _need(n_vis, "n_vis", torch.int32, B, Q)
-    if out.data_ptr() == q.data_ptr():
-        raise ValueError("out must not be q: several CTAs read a query while others already write")
     if lse is not None:
         _need(lse, "lse", torch.float32, B, Q, 64)
     fp4 = kv.dtype == torch.uint8
@@ -464,6 +479,10 @@ def paged_attn_args(q, kv, block_table, n_vis, out, lse=None, swa=None, W=0, swa
         _need(swa, "swa", torch.bfloat16 if swa_scale is None else torch.uint8, B, None, 512)
         if swa_scale is not None:
             _need(swa_scale, "swa_scale", torch.float32, B, swa.shape[1])
+    inputs = dict(q=q, kv=kv, block_table=block_table, n_vis=n_vis, swa=swa if W else None, swa_scale=swa_scale if W else None)
+    _need_apart(out, "out", lse=lse, **inputs)
+    if lse is not None:
+        _need_apart(lse, "lse", **inputs)
     stride = kv.stride(0) if kv.shape[0] > 1 else kv.shape[1] * width
     a = PagedAttnArgs(B=B, Q=Q, W=W, block_size=kv.shape[1], max_blocks=max_blocks, ld_table=ld, n_blocks=kv.shape[0],
                       block_stride=stride * kv.element_size(), q=_ptr(q), kv=_ptr(kv),

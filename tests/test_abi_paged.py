@@ -181,3 +181,41 @@ def test_output_over_the_queries_is_refused():
     csa2.paged_attn_args(q, kv, table, vis, torch.zeros_like(q))
     with pytest.raises(ValueError, match="out must not be q"):
         csa2.paged_attn_args(q, kv, table, vis, q)
+
+
+def test_outputs_that_share_bytes_with_inputs_are_refused():
+    """Anywhere, not only at the start; what lies between a pool's blocks is not the pool."""
+    buf = torch.zeros(1 << 21, dtype=torch.uint8)
+    at = lambda first, dtype, *shape: buf[first: first + torch.Size(shape).numel() * dtype.itemsize].view(dtype).view(shape)
+    n = 2 * 64 * 512 * 2                                 # bytes of q and of out
+    q, table, vis = at(0, torch.bfloat16, 2, 1, 64, 512), at(n, torch.int32, 2, 3), at(n + 32, torch.int32, 2, 1)
+    kv = at(4 * n, torch.uint8, 6, 4, 288)
+    far = lambda: torch.zeros(2, 1, 64, 512, dtype=torch.bfloat16)
+    lse = lambda: torch.zeros(2, 1, 64)
+    args = csa2.paged_attn_args
+    args(q, kv, table, vis, at(n + 48, torch.bfloat16, 2, 1, 64, 512), at(4 * n - 512, torch.float32, 2, 1, 64))
+    for first, what in ((n - 16, "q"), (16, "q"), (n + 16, "block_table"), (n + 32, "n_vis"), (4 * n - 16, "kv"),
+                        (4 * n + 6 * 4 * 288 - 16, "kv")):
+        with pytest.raises(ValueError, match=f"out must not be {what}"):
+            args(q, kv, table, vis, at(first, torch.bfloat16, 2, 1, 64, 512))
+    for first, what in ((n - 16, "q"), (n + 16, "block_table"), (4 * n - 16, "kv")):
+        with pytest.raises(ValueError, match=f"lse must not be {what}"):
+            args(q, kv, table, vis, far(), at(first, torch.float32, 2, 1, 64))
+    out = far()
+    with pytest.raises(ValueError, match="out must not be lse"):
+        args(q, kv, table, vis, out, out.view(-1).view(torch.float32)[64:192].view(2, 1, 64))
+    swa = torch.zeros(2, 128, 512, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="out must not be swa"):
+        args(q, kv, table, vis, swa[:1].view(2, 1, 64, 512), swa=swa, W=128)
+    codes, scale = torch.zeros(2, 128, 512, dtype=torch.uint8), torch.zeros(2, 128)
+    with pytest.raises(ValueError, match="lse must not be swa_scale"):
+        args(q, kv, table, vis, far(), scale.view(-1)[128:].view(2, 1, 64), swa=codes, W=128, swa_scale=scale)
+    # blocks of two layers in one pool, and a log-sum-exp in the gap
+    wide = torch.zeros(6, 2, 4, 288, dtype=torch.uint8)
+    gap = lambda i, first: wide[i].view(-1)[first: first + 512].view(torch.float32).view(2, 1, 64)
+    args(q, wide[:, 0], table, vis, far(), gap(2, 4 * 288))
+    args(q, wide[:, 0], table, vis, far(), gap(5, 4 * 288 + 512))
+    args(q, wide[:, 1], table, vis, far(), gap(0, 0))
+    for i, first in ((0, 4 * 288 - 16), (2, 4 * 288 - 512), (5, 0)):
+        with pytest.raises(ValueError, match="lse must not be kv"):
+            args(q, wide[:, 0], table, vis, far(), gap(i, first))
