@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from fp4_kv_cache_mxfp4_b200 import csa2
-from oracle import fp4
-from parity import f32
+from oracle import attention, fp4
+from parity import check_attention, f32
 from test_gpu_paged import Case
 
 pytestmark = pytest.mark.gpu
@@ -179,3 +179,105 @@ def test_logits_below_the_range_of_float32(lens, far):
     c.run()
     c.vis = np.maximum(c.vis - far, 0)
     c.check([(b, 0) for b in range(0, len(lens), 13)])
+
+
+# ---------------------------------------------------------------------------
+# every key, the log-sum-exp's own precision, prompts, the largest batch
+# ---------------------------------------------------------------------------
+
+def _one_dim_each(n):
+    """n rows with one value each: consecutive rows share a dim, the first of them in dim 0."""
+    x = torch.zeros(n, 512)
+    j = torch.arange(n)
+    x[j, j * 512 // n] = 1.0 + 0.5 * (j % 5)
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("kv", ["fp4", "bf16"])
+@pytest.mark.parametrize("lens,block,W,window", [
+    ([20000], 64, 0, "bf16"), ([4000, 1, 600, 9000], 7, 0, "bf16"), ([128 * 9] * 200, 128, 0, "bf16"),
+    ([0, 700], 32, 1024, "bf16"), ([700, 0], 32, 1000, "fp8"),
+])
+def test_every_key_counts(lens, block, W, window, kv):
+    """A dim of the output is the weight of at most 40 keys: one of them lost,
+    or read as its neighbour tile's, changes it by more than the tolerance, 3 * 2^-8 of it."""
+    c = Case(lens, 1, block, W, kv, window, seed=80)
+    for b, n in enumerate(lens):
+        if not n:
+            continue
+        x = _one_dim_each(n)
+        raw = torch.from_numpy(fp4.quantize_kv_fp4(f32(x))) if kv == "fp4" else x
+        c.keys[b] = fp4.dequantize_kv_fp4(raw.numpy()) if kv == "fp4" else f32(x).astype(np.float64)
+        j = np.arange(n)
+        c.pool[c.table[b, j // block], j % block] = raw.cuda()
+    if W:
+        x = _one_dim_each(W)
+        c.win[:] = f32(x)
+        if window == "fp8":
+            s = x.float().abs().amax(1) / 256               # 256 times the row: exact codes and scales
+            c.swa[:] = (x.float() / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+            c.swa_scale[:] = s.cuda()
+        else:
+            c.swa[:] = x.cuda()
+    c.run().check([(b, 0) for b in range(0, len(lens), max(1, len(lens) // 8))] + [(len(lens) - 1, 0)])
+
+
+@pytest.mark.parametrize("kv", ["fp4", "bf16"])
+@pytest.mark.parametrize("W,window", [(0, "bf16"), (7, "bf16"), (5, "fp8")])
+def test_log_sum_exp_keeps_float32(kv, W, window):
+    """Queries with 8 channels, so that logits are nearly exact and the sum
+    itself is tested: 8 products, each added with at most one unit of
+    float32's last place lost, 2^-23; the logit's and the exponential's own
+    roundings; float32 sums over a thread's tiles, the lanes and the
+    parts (fewer than 64 steps beside the tiles).  Weights rounded to bf16
+    would be off by up to 2^-9."""
+    lens = [1, 2, 3, 5, 17, 130, 700, 3000]
+    c = Case(lens, 1, 16, W, kv, window, seed=81, q_std=3.0, scale=0.5)
+    c.q[..., 8:] = 0
+    c.q_d.copy_(c.q)
+    c.run().check()
+    for b in range(len(lens)):
+        keys, q = c._visible(b, 0), f32(c.q[b, 0]).astype(np.float64)
+        z = q @ keys.T * 0.5
+        m = z.max(1)
+        want = m + np.log(np.exp(z - m[:, None]).sum(1))
+        e = 8 * 2.0 ** -23 * 0.5 * (np.abs(q) @ np.abs(keys).T).max(1) + 2.0 ** -22 * np.abs(z).max(1)
+        tol = e + (len(keys) / 128 + 64) * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * np.abs(want)
+        err = np.abs(c.lse[b, 0].cpu().numpy() - want)
+        assert np.all(err <= tol), f"request {b}: {np.max(err / tol):.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("kv", ["fp4", "bf16"])
+@pytest.mark.parametrize("n,Q,W", [(700, 300, 16), (260, 260, 0), (1500, 130, 128)])
+def test_a_prompt(n, Q, W, kv):
+    """Many query positions of one request, causal, the first ones with few keys."""
+    c = Case([n], Q, 32, W, kv, seed=82).run()
+    c.check([(0, i) for i in range(0, Q, 7)] + [(0, Q - 1)])
+
+
+def test_the_largest_batch():
+    """65,535 queries: 4.3 GB of Q and of results."""
+    B, P = 65535, 64
+    g = torch.Generator().manual_seed(83)
+    x = torch.randn(P, 512, generator=g).to(torch.bfloat16)
+    raw = fp4.quantize_kv_fp4(f32(x))
+    keys = fp4.dequantize_kv_fp4(raw)
+    base = torch.randn(3, 64, 512, generator=g).to(torch.bfloat16)
+    which = torch.arange(B, device="cuda") % 3
+    q = base.cuda()[which].view(B, 1, 64, 512)
+    vis = (torch.arange(B, dtype=torch.int32, device="cuda") % 61)[:, None].contiguous()
+    out, lse = torch.full_like(q, float("nan")), torch.full((B, 1, 64), float("nan"), device="cuda")
+    args = csa2.paged_attn_args(q, torch.from_numpy(raw).cuda().view(1, P, 288),
+                                torch.zeros(B, 1, dtype=torch.int32, device="cuda"), vis, out, lse)
+    csa2.csa2_paged_attn(args, csa2.workspace(args, csa2.WS_PAGED_ATTN))
+    torch.cuda.synchronize()
+    assert csa2.csa2_device_status() == (0, 0)
+    for b in list(range(0, B, 1009)) + [B - 1]:
+        n = b % 61
+        o, l = attention.sparse_mqa(f32(base[b % 3]), keys, np.arange(n), np.zeros((0, 512)))
+        check_attention(out[b, 0], o, what=f"query {b}")
+        # 512 products in float32, 512 * 2^-24 * scale * sum |q k|, below 1e-3 for these inputs
+        assert np.allclose(lse[b, 0].cpu().numpy(), l, rtol=0, atol=1e-3)
+    # equal inputs, equal bits: every query against the one 183 places before it, cut ones (one per CTA at most) apart
+    same = (out[183:].view(B - 183, -1) == out[:-183].view(B - 183, -1)).all(1)
+    assert int((~same).sum()) <= 2 * 148
