@@ -15,20 +15,26 @@
 //                                  CTA order (a fixed order: results do not
 //                                  depend on timing)
 // A CTA has at most two partials: its first query (when that began in an
-// earlier range) and its last (when that goes on).
+// earlier range) and its last (when that goes on).  Runs of one part of a query
+// (kPagedRun) are merged in the same two places.
 //
 // Mathematics of a tile, as in attention_tc.cuh: S^T[key, head] = K . Q^T
 // (tcgen05, M = 128 keys, N = 64 heads, K = 512 dims), weights
 // P^T = exp2(S^T - ref) in bf16 against a running reference per head that
 // moves only when a logit passes it by 2^8, O^T[dim, head] += V^T . P^T
 // (M = 128 dims x 4, N = 64, K = 128 keys) with the same bf16 key tile read
-// along its other axis.
+// along its other axis.  The weights are the one thing rounded before the end:
+// an MMA's operands have one type, and as TF32 keys and weights would take
+// twice the shared memory and half the rate.  A weight is off by up to 2^-8 of itself,
+// the output by 2.2e-3 of its norm at most (1.7e-3 for the bf16 result alone);
+// the sums that divide it are of the unrounded weights, in float32.
 //
 // What bounds it: the data path of shared memory and L1.  A tile's 64 MMAs
 // read 6 KB of operands each at 128 B per cycle, 48 cycles (measured; the MMA
 // rate alone would allow 32), half of a tile; beside them the expanded keys are
 // written (1024 cycles) and raw keys, weights and addresses pass, 3100
-// load/store wavefronts per tile in all (counted).  One key tile (128 KB), Q
+// load/store wavefronts per tile in all (counted; half of them are not shared
+// memory: scales read two bytes at a time and prefetches of rows).  One key tile (128 KB), Q
 // (64 KB) and P^T (16 KB) fill the shared memory, so there is no second tile to work on while the
 // softmax runs (some 1300 cycles, 512 of them the exponentials' rate); the
 // tile is filled in slabs of 128 dims instead: MMA 2 releases slab t when its
@@ -49,8 +55,8 @@
 //                wait in registers; bf16 rows go by cp.async)
 //   warps 12-27  softmax: S^T from tensor memory, weights to P^T, and the
 //                epilogue; warp w has keys 32 (w % 4).. and heads 16 (w / 4 - 3)..
-// Every role about fits in the 72 registers that 28 warps leave each thread
-// (40 bytes are spilled; what of that lies in the loops costs: 58 bytes cost 11 %): with the whole
+// Every role fits in the 72 registers that 28 warps leave each thread (8
+// bytes are spilled).  Spills in the loops cost (58 bytes: 11 %): with the whole
 // shared memory taken, L1 is too small for spilled values to stay, and each
 // reload then costs an L2 round trip.
 //

@@ -107,7 +107,9 @@ typedef enum csa2_mode {
  *   kv_fp4    u8 cache rows of CSA2_ENTRY_BYTES bytes
  *   dst_rows  optional int64 [n]: entry i goes to row dst_rows[i], or
  *             nowhere when that is negative (the padding of
- *             csa2_block_tables); NULL means row row_offset + i
+ *             csa2_block_tables, and libraries that export it: earlier ones
+ *             of the same csa2_version() wrote before the cache); NULL
+ *             means row row_offset + i
  *   row_offset  first destination row when dst_rows is NULL, >= 0
  * Entries map to distinct rows (overlapping destinations race).  The call
  * does not know the cache's size: every destination row must lie inside
@@ -588,7 +590,10 @@ csa2_status csa2_paged_rows(const csa2_paged_rows_args* a, void* stream);
  * Entries in a block that the table does not name (an id outside
  * [0, n_blocks)) are no keys; rows of the pool that no visible entry lies in
  * are not read, whatever they hold.  A query with no key gets out = 0 and
- * lse = -inf.  A block may stand in several rows of the table (a shared
+ * lse = -inf.  A logit beyond float32 has weight 0 when it is negative; any
+ * other value that is not finite makes its query's head NaN, lse too.  (The
+ * E4M3 scale codes 0x7F and 0xFF, which the quantiser never writes, read as
+ * +-480.)  A block may stand in several rows of the table (a shared
  * prefix).  out and lse must not overlap any input: several CTAs read a
  * query while others already write.
  *
@@ -599,7 +604,13 @@ csa2_status csa2_paged_rows(const csa2_paged_rows_args* a, void* stream);
  *
  * The keys of all queries together are cut into equal pieces, one per SM,
  * whatever the lengths; queries that a cut divides are joined from fp32
- * partials in the workspace, always in the same order.
+ * partials in the workspace, always in the same order.  A piece of any
+ * length is summed in runs of 32,768 keys, so that the error does not grow
+ * with it.  Softmax weights are rounded to bf16 for the tensor cores (2^-8
+ * of each at most); their sum, the maxima and all output sums are fp32.
+ * Not offered: quantised Q (q_format of csa2_attn_args), index-K in blocks,
+ * and a pool in csa2_group_decode and csa2_stack_decode, whose caches are
+ * dense.
  * ---------------------------------------------------------------------- */
 typedef struct csa2_paged_attn_args {
     int32_t        B, Q;        /* B * Q <= CSA2_MAX_BQ                          */
