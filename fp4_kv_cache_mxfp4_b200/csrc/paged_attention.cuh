@@ -26,7 +26,7 @@
 // along its other axis.  The weights are the one thing rounded before the end:
 // an MMA's operands have one type, and as TF32 keys and weights would take
 // twice the shared memory and half the rate.  A weight is off by up to 2^-8 of itself,
-// the output by 2.2e-3 of its norm at most (1.7e-3 for the bf16 result alone);
+// the output by 2.3e-3 of its norm at most (1.7e-3 for the bf16 result alone);
 // the sums that divide it are of the unrounded weights, in float32.
 //
 // What bounds it: the data path of shared memory and L1.  A tile's 64 MMAs
