@@ -801,9 +801,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, PagedAttnParams p)
         if (!KVB && window) rs *= kPagedFp4Down;
         paged_wait(s_full, it & 1, kErrWaitTmemFull, abort_flag);
         tc_fence_after();
-        // y = exp2(logit - reference) in log2 units.  The weights go to P^T before the vote on whether some
-        // reference must move (then they are made again), and into the sums
-        // after the hand-over: both off the path from S^T to MMA 2.
+        // y = exp2(logit - reference) in log2 units.  The weights go to P^T before
+        // the vote on whether some reference must move (then they are made again),
+        // and into the sums after the hand-over: both off the path from S^T to MMA 2.
         float y[16];
         float over = -INFINITY;
         auto weights = [&]() {
